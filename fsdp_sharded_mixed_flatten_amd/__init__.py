@@ -1,7 +1,7 @@
 """Python binding of ``libzs.so``, the MI355X shard-local step (ZeRO / FSDP).
 
 Argument marshalling only: every step of the path runs in the library's HIP
-kernels. Functions carry the C ABI's names (``include/zs.h``). Device buffers
+kernels. Functions carry the C ABI's names (``include/zs.h``, ``include/zs_lm.h``). Device buffers
 are PyTorch CUDA tensors (or raw integer device addresses); the stream is
 ``torch.cuda.current_stream()`` unless one is given. Before each call the
 binding checks that every tensor is a contiguous CUDA tensor of the right
@@ -22,6 +22,10 @@ ZS_OK, ZS_EINVAL, ZS_EALIGN, ZS_ERANGE, ZS_EHIP, ZS_ENOMEM = 0, -1, -2, -3, -4, 
 ZS_LAYOUT_FLAT, ZS_LAYOUT_PER_TENSOR = 0, 1
 ZS_MAX_CONTRIBS = 256
 ZS_MAX_GROUPS = 8
+ZS_DTYPE_BF16, ZS_DTYPE_F32 = 0, 1
+ZS_QUANT_MATVEC_MAX_ROWS = 64
+ZS_LOGPROBS_MAX_TOP = 32
+ZS_DISTILL_MAX_K = 1024
 GRAD_STATS_NOALLOC_MAX_ELEMS = 1431568384
 FUSED_TWO_PASS_MIN_CONTRIBS = 52  # zs_fused_shard_step runs two passes from here when grad is given
 
@@ -144,6 +148,10 @@ def _load():
         "zs_adamw_shard_step_dc": (st, [vp, vp, vp, vp, vp, vp, vp, vp]),
         "zs_adamw_shard_step_accum_dc": (st, [vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]),
         "zs_fused_shard_step_multi_dc": (st, [vp, vp, i32, vp, vp]),
+        "zs_quant_matvec": (st, [vp, i32, i64, i64, i32, i32, vp, vp, vp, i64, i32, vp, i32, i64, vp]),
+        "zs_token_logprobs": (st, [vp, i32, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, i32, vp, vp, vp]),
+        "zs_token_logprobs_backward": (st, [vp, i32, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, i64, vp]),
+        "zs_distill_topk": (st, [vp, i32, i64, i64, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64, vp]),
         "zs_last_error": (ctypes.c_char_p, []),
         "zs_version": (ctypes.c_char_p, []),
     }
@@ -172,6 +180,8 @@ EXPORTED = ("zs_shard_plan", "zs_shard_plan_ex", "zs_plan_tensor_group", "zs_pla
             "zs_adamw_coefs_compute",
             "zs_fused_shard_step_dc", "zs_adamw_shard_step_dc", "zs_adamw_shard_step_accum_dc",
             "zs_fused_shard_step_multi_dc", "zs_last_error", "zs_version")
+# the language-model operators (include/zs_lm.h)
+EXPORTED_LM = ("zs_quant_matvec", "zs_token_logprobs", "zs_token_logprobs_backward", "zs_distill_topk")
 
 
 def lib():
@@ -697,6 +707,152 @@ def zs_adamw_shard_step_accum_dc(plan, coefs, acc, grad_divisor, master, m, v, s
 def zs_fused_shard_step_multi_dc(plan, coefs, n_groups, workspace, stream=None):
     _check(_lib.zs_fused_shard_step_multi_dc(plan.handle, _coefs_ptr(coefs, n_groups), n_groups,
                                              workspace.data_ptr(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- language-model operators
+
+
+def _lm_device(t, what):
+    """The device of the call: that of its first tensor. The language-model
+    calls run on this device's current stream, whichever device is current."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
+
+
+def _lm_rows(t, dtypes, rows, cols, device, what):
+    """(address, row stride) of a [rows, cols] matrix whose rows are contiguous."""
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's first tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows, its strides are {t.stride()}")
+    # the stride of a single row is free, and may be anything in torch
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _lm_array(t, dtype, shape, device, what):
+    """Address of a contiguous array of exactly this shape, or None."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's first tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _lm_call(fn, device, stream, *args):
+    """Runs fn(*args, stream) with the call's device current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if not isinstance(stream, int):
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
+def _lm_logits(logits):
+    """(device, dtype code, address, rows, vocab, row stride) of a [rows, vocab] matrix of logits."""
+    import torch
+    device = _lm_device(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, vocab], got {list(logits.shape)}")
+    rows, vocab = logits.shape
+    ptr, stride = _lm_rows(logits, (torch.bfloat16, torch.float32), rows, vocab, device, "logits")
+    return device, ZS_DTYPE_BF16 if logits.dtype == torch.bfloat16 else ZS_DTYPE_F32, ptr, rows, vocab, stride
+
+
+def zs_quant_matvec(plan, tensor, out_features, in_features, bits, block, codes_all, scales_all, x, y, stream=None):
+    """y[r, o] = sum_i W[o, i] x[r, i] with W = tensor `tensor` of the plan (out_features x in_features) read from
+    the quantized gather's payload. x: bfloat16 [rows, in_features]; y: bfloat16 or float32 [rows, out_features]."""
+    import torch
+    device = _lm_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, {in_features}], got {list(x.shape)}")
+    rows = x.shape[0]
+    xp, xs = _lm_rows(x, (torch.bfloat16,), rows, in_features, device, "x")
+    yp, ys = _lm_rows(y, (torch.bfloat16, torch.float32), rows, out_features, device, "y")
+    S, N = plan.shard_numel, plan.world_size
+    for t, what in ((codes_all, "codes_all"), (scales_all, "scales_all")):
+        if not isinstance(t, int) and t.device != device:
+            raise ValueError(f"{what} is on {t.device}, x on {device}")
+    _lm_call(_lib.zs_quant_matvec, device, stream, plan.handle, tensor, out_features, in_features, bits, block,
+             _ptr(codes_all, "bytes", N * S * bits // 8, "codes_all"),
+             _ptr(scales_all, "f32", N * -(-S // max(block, 1)), "scales_all"), xp, xs, rows, yp,
+             ZS_DTYPE_BF16 if y.dtype == torch.bfloat16 else ZS_DTYPE_F32, ys)
+
+
+def zs_token_logprobs(logits, tokens, temperature=1.0, logprob=None, entropy=None, stats=None, top_ids=None,
+                      top_logprobs=None, stream=None):
+    """logits: bfloat16 or float32 [rows, vocab]; tokens: int32 [rows]. Outputs, each optional: logprob and entropy
+    float32 [rows]; stats float32 [rows, 2], which the gradient takes; top_ids int32 and top_logprobs float32
+    [rows, top], together."""
+    import torch
+    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs are given together")
+    top = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError(f"top_ids must be [{rows}, top], got {list(top_ids.shape)}")
+        top = top_ids.shape[1]
+    if top == 0:
+        top_ids = top_logprobs = None
+    _lm_call(_lib.zs_token_logprobs, device, stream, ptr, dtype, rows, vocab, stride,
+             _lm_array(tokens, torch.int32, (rows,), device, "tokens"), temperature,
+             _lm_array(logprob, torch.float32, (rows,), device, "logprob"),
+             _lm_array(entropy, torch.float32, (rows,), device, "entropy"),
+             _lm_array(stats, torch.float32, (rows, 2), device, "stats"), top,
+             _lm_array(top_ids, torch.int32, (rows, top), device, "top_ids"),
+             _lm_array(top_logprobs, torch.float32, (rows, top), device, "top_logprobs"))
+
+
+def zs_token_logprobs_backward(logits, tokens, stats, grad_logprob, grad_logits, temperature=1.0, entropy=None,
+                               grad_entropy=None, stream=None):
+    """grad_logits (the logits' dtype; logits itself for in place) from the forward call's stats and the gradients of
+    logprob and, with the forward call's entropy, of entropy."""
+    import torch
+    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
+    gp, gs = _lm_rows(grad_logits, (logits.dtype,), rows, vocab, device, "grad_logits")
+    _lm_call(_lib.zs_token_logprobs_backward, device, stream, ptr, dtype, rows, vocab, stride,
+             _lm_array(tokens, torch.int32, (rows,), device, "tokens"), temperature,
+             _lm_array(stats, torch.float32, (rows, 2), device, "stats"),
+             _lm_array(entropy, torch.float32, (rows,), device, "entropy"),
+             _lm_array(grad_logprob, torch.float32, (rows,), device, "grad_logprob"),
+             _lm_array(grad_entropy, torch.float32, (rows,), device, "grad_entropy"), gp, gs)
+
+
+def zs_distill_topk(logits, teacher_ids, teacher_logits, loss, grad_logits=None, temperature=1.0, row_weight=None,
+                    stream=None):
+    """Distillation loss [rows] (float32) from the teacher's top entries (teacher_ids int32, teacher_logits float32,
+    both [rows, k]; a negative id is unused) and, if given, its gradient grad_logits (the logits' dtype; logits itself
+    for in place)."""
+    import torch
+    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
+    if teacher_ids.dim() != 2:
+        raise ValueError(f"teacher_ids must be [{rows}, k], got {list(teacher_ids.shape)}")
+    k = teacher_ids.shape[1]
+    gp, gs = None, vocab
+    if grad_logits is not None:
+        gp, gs = _lm_rows(grad_logits, (logits.dtype,), rows, vocab, device, "grad_logits")
+    _lm_call(_lib.zs_distill_topk, device, stream, ptr, dtype, rows, vocab, stride,
+             _lm_array(teacher_ids, torch.int32, (rows, k), device, "teacher_ids"),
+             _lm_array(teacher_logits, torch.float32, (rows, k), device, "teacher_logits"), k, temperature,
+             _lm_array(row_weight, torch.float32, (rows,), device, "row_weight"),
+             _lm_array(loss, torch.float32, (rows,), device, "loss"), gp, gs)
 
 
 def zs_last_error():

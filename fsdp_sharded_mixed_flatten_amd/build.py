@@ -1,7 +1,8 @@
 """Builds the shard-step library libzs.so for gfx950, in-tree.
 
 Host code (plan, validation, the host AdamW of the offloaded step) is C++17;
-kernels and the offload pipeline are HIP compiled for gfx950. Everything is
+kernels (the step's and the language-model operators') and the offload
+pipeline are HIP compiled for gfx950. Everything is
 built with contraction off (the element arithmetic must round operation by
 operation); HIP code also with packed-fp32 instruction generation disabled.
 """
@@ -38,16 +39,17 @@ def build(verbose=False, out=None):
     """Builds libzs.so (or ``out``)."""
     os.makedirs(BUILD, exist_ok=True)
     objs = []
-    api_o = os.path.join(BUILD, "zs_api.o")
-    _run(["g++", *COMMON, "-c", os.path.join(CSRC, "zs_api.cpp"), "-o", api_o], verbose)
-    objs.append(api_o)
+    for name in ("zs_api", "zs_lm_api"):
+        o = os.path.join(BUILD, f"{name}.o")
+        _run(["g++", *COMMON, "-c", os.path.join(CSRC, f"{name}.cpp"), "-o", o], verbose)
+        objs.append(o)
     host_o = os.path.join(BUILD, "zs_host_adamw.o")
     # host AdamW: same one-rounding-per-operation rule; -fno-math-errno lets
     # sqrtf become the (correctly rounded) vector instruction
     _run(["g++", *COMMON, "-fno-math-errno", "-pthread", "-c", os.path.join(CSRC, "zs_host_adamw.cpp"), "-o",
           host_o], verbose)
     objs.append(host_o)
-    for name in ("zs_kernels", "zs_offload"):
+    for name in ("zs_kernels", "zs_offload", "zs_matvec", "zs_loss"):
         o = os.path.join(BUILD, f"{name}.o")
         _run([HIPCC, *COMMON, *HIP_ONLY, "-c", os.path.join(CSRC, f"{name}.hip"), "-o", o], verbose)
         objs.append(o)

@@ -122,6 +122,30 @@ std::unordered_map<const void*, Binding> g_bind;
 
 }  // namespace
 
+// For the other host files of the library (zs_lm_internal.h).
+namespace zs {
+
+zs_status report(zs_status st, const char* fmt, ...);
+zs_status report_hip(int err, const char* what);
+void trace_call(const char* op, const zs_plan* p, int32_t n_contribs, int64_t off, int64_t len, const void* stream);
+
+zs_status report(zs_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(st, "%s", buf);
+}
+
+zs_status report_hip(int err, const char* what) { return hip_status(err, what); }
+
+void trace_call(const char* op, const zs_plan* p, int32_t n_contribs, int64_t off, int64_t len, const void* stream) {
+    trace(op, p, n_contribs, off, len, stream);
+}
+
+}  // namespace zs
+
 namespace zs {
 
 AdamCoef make_coef(const zs_adamw_hparams& hp) {

@@ -1,0 +1,536 @@
+// Losses over rows of logits for CDNA4 (gfx950): log-probabilities of given
+// tokens with entropy and the best alternatives, their gradient, and
+// distillation from a teacher's top logits with its gradient.
+//
+// Every kernel is a stream over rows of `vocab` logits (2 or 4 bytes each)
+// with one exponential and a few fp32 operations an element. Differences
+// from the row's maximum are taken of the logits themselves, before the
+// temperature scales them, so values near the type's ends neither overflow nor
+// lose their order; exponentials are powers of two of differences scaled by
+// log2(e) / temperature.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "zs_lm_internal.h"
+
+namespace zs {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes at any multiple of the element's size: rows of an odd stride start
+// anywhere (the hardware takes unaligned vector accesses).
+typedef u32x4 __attribute__((aligned(2))) u32x4_u2;
+
+constexpr float kInf = __builtin_inff();
+constexpr float kLn2 = 0.693147180559945309f;
+// Differences d are bounded below by this where they multiply 2^d, which is 0
+// long before (and the products stay far from infinity).
+constexpr float kLowest = -1.0e4f;
+
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
+
+// fp32 -> bf16 bits, round to nearest even (the one rounding of a stored
+// gradient); NaN stays NaN.
+__device__ __forceinline__ uint32_t f32_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+    return ((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r;
+}
+
+// A 16-byte vector of logits as fp32 values and back.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ float get(const u32x4& v, int i) {
+        return __uint_as_float((i & 1) ? (v[i >> 1] & 0xFFFF0000u) : (v[i >> 1] << 16));
+    }
+    static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+    static __device__ __forceinline__ uint16_t round(float f) { return (uint16_t)f32_bf16(f); }
+    static __device__ __forceinline__ u32x4 pack(const float* f) {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f32_bf16(f[2 * i]) | (f32_bf16(f[2 * i + 1]) << 16);
+        return v;
+    }
+    static constexpr uint32_t kNegInf = 0xFF80FF80u;
+};
+template <>
+struct Vec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ float get(const u32x4& v, int i) { return __uint_as_float(v[i]); }
+    static __device__ __forceinline__ float one(float x) { return x; }
+    static __device__ __forceinline__ float round(float f) { return f; }
+    static __device__ __forceinline__ u32x4 pack(const float* f) {
+        return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    }
+    static constexpr uint32_t kNegInf = 0xFF800000u;
+};
+
+template <typename T>
+__device__ __forceinline__ u32x4 load_vec(const T* p) {
+    return *reinterpret_cast<const u32x4_u2*>(p);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, u32x4 v) {
+    *reinterpret_cast<u32x4_u2*>(p) = v;
+}
+
+// ------------------------------------------------------------------ running softmax
+// max m of the logits, s = sum of 2^((x - m) k) and t = sum of 2^d d with
+// d = (x - m) k, k = log2(e) / temperature. d is bounded below in the product
+// so that masked logits (d = -infinity, 2^d = 0) add 0; a NaN, or a difference
+// of two infinities, makes s NaN.
+struct Running {
+    float m, s, t;
+};
+
+// m, or 0 where nothing has been seen yet (m = -infinity).
+__device__ __forceinline__ float base_of(float m) { return m == -kInf ? 0.0f : m; }
+
+// Moves r to the maximum m (>= r.m).
+__device__ __forceinline__ void rebase(Running& r, float m, float k) {
+    const float d = (r.m - base_of(m)) * k;
+    const float c = exp2f(d);
+    r.t = c * (r.t + r.s * fmaxf(d, kLowest));
+    r.s = c * r.s;
+    r.m = m;
+}
+
+__device__ __forceinline__ Running merge(Running a, Running b, float k) {
+    const float m = fmaxf(a.m, b.m);
+    rebase(a, m, k);
+    rebase(b, m, k);
+    return Running{m, a.s + b.s, a.t + b.t};
+}
+
+__device__ __forceinline__ void add_one(Running& r, float x, float k) {
+    const float m = fmaxf(r.m, x);
+    rebase(r, m, k);
+    const float d = (x - base_of(m)) * k;
+    const float e = exp2f(d);
+    r.s += e;
+    r.t += e * fmaxf(d, kLowest);
+}
+
+// The block's Running from its threads', the same in every thread. THREADS / 64
+// entries of `part`, which may be used again after the next barrier.
+template <int THREADS>
+__device__ __forceinline__ Running block_merge(Running r, float k, Running* part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const Running o{__shfl_xor(r.m, d, 64), __shfl_xor(r.s, d, 64), __shfl_xor(r.t, d, 64)};
+        r = merge(r, o, k);
+    }
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = r;
+    __syncthreads();
+    r = part[0];
+    for (int w = 1; w < THREADS / 64; ++w) r = merge(r, part[w], k);
+    return r;
+}
+
+// One thread's share of a row: vectors tid, tid + THREADS, ... and one element
+// of the tail behind the last whole vector.
+template <typename T, int THREADS, int U>
+__device__ __forceinline__ Running row_running(const T* __restrict__ row, int64_t vocab, float k) {
+    constexpr int N = Vec<T>::kN;
+    const int64_t nv = vocab / N;
+    Running r{-kInf, 0.0f, 0.0f};
+    for (int64_t v0 = threadIdx.x; v0 < nv; v0 += (int64_t)THREADS * U) {
+        u32x4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t v = v0 + (int64_t)u * THREADS;
+            const uint32_t none = Vec<T>::kNegInf;
+            x[u] = v < nv ? load_vec(row + v * N) : u32x4{none, none, none, none};
+        }
+        float m = r.m;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = fmaxf(m, Vec<T>::get(x[u], i));
+        rebase(r, m, k);
+        const float b = base_of(m);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float s = 0.0f, t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float d = (Vec<T>::get(x[u], i) - b) * k;
+                const float e = exp2f(d);
+                s += e;
+                t += e * fmaxf(d, kLowest);
+            }
+            r.s += s;
+            r.t += t;
+        }
+    }
+    const int64_t tail = nv * N + threadIdx.x;
+    if (tail < vocab) add_one(r, Vec<T>::one(row[tail]), k);
+    return r;
+}
+
+// ------------------------------------------------------------------ best alternatives
+
+// Whether logit a of token i comes before logit b of token j.
+__device__ __forceinline__ bool before(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
+
+// The thread's first element that comes after (x0, i0) in the order of
+// `before`; token INT32_MAX if there is none.
+template <typename T, int THREADS>
+__device__ __forceinline__ void next_own(const T* __restrict__ row, int64_t vocab, float x0, int i0, float* best,
+                                         int* best_i) {
+    constexpr int N = Vec<T>::kN;
+    const int64_t nv = vocab / N;
+    float b = -kInf;
+    int bi = INT32_MAX;
+    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
+        const u32x4 x = load_vec(row + v * N);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float f = Vec<T>::get(x, i);
+            const int at = (int)(v * N) + i;
+            if (before(x0, i0, f, at) && before(f, at, b, bi)) {
+                b = f;
+                bi = at;
+            }
+        }
+    }
+    const int64_t tail = nv * N + threadIdx.x;
+    if (tail < vocab) {
+        const float f = Vec<T>::one(row[tail]);
+        if (before(x0, i0, f, (int)tail) && before(f, (int)tail, b, bi)) {
+            b = f;
+            bi = (int)tail;
+        }
+    }
+    *best = b;
+    *best_i = bi;
+}
+
+// The row's `top` best elements by rounds: every thread holds the best of its
+// own elements that has not been taken, the best of those is taken, and the
+// thread it came from looks for its next. Right for any row (equal or masked
+// logits included). Every logit is below +infinity and no NaN.
+template <typename T, int THREADS>
+__device__ __forceinline__ void top_by_rounds(const T* __restrict__ row, int64_t vocab, int top, float m, float inv_t,
+                                              float logsum, int32_t* ids, float* lps, float* lx, int* li) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float b;
+    int bi;
+    next_own<T, THREADS>(row, vocab, kInf, -1, &b, &bi);
+    for (int n = 0; n < top; ++n) {
+        float x = b;
+        int i = bi;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            const float ox = __shfl_xor(x, d, 64);
+            const int oi = __shfl_xor(i, d, 64);
+            if (before(ox, oi, x, i)) {
+                x = ox;
+                i = oi;
+            }
+        }
+        if (lane == 0) {
+            lx[wave] = x;
+            li[wave] = i;
+        }
+        __syncthreads();
+        for (int w = 0; w < THREADS / 64; ++w)
+            if (before(lx[w], li[w], x, i)) {
+                x = lx[w];
+                i = li[w];
+            }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            ids[n] = i;
+            lps[n] = m == -kInf ? -kInf : (x - m) * inv_t - logsum;
+        }
+        if (bi == i) next_own<T, THREADS>(row, vocab, x, i, &b, &bi);
+    }
+}
+
+// ------------------------------------------------------------------ log-probabilities
+
+constexpr int kRowThreads = 256;
+
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logits, int64_t stride, int64_t vocab,
+                                                      const int32_t* __restrict__ tokens, float inv_t, float k,
+                                                      LogprobsOut out) {
+    __shared__ Running part[THREADS / 64];
+    __shared__ float lx[THREADS / 64];
+    __shared__ int li[THREADS / 64];
+    const int64_t r = blockIdx.x;
+    const T* row = logits + r * stride;
+    const int64_t token = tokens[r];
+    int32_t* ids = out.top_ids + r * out.top;
+    float* lps = out.top_logprobs + r * out.top;
+    if (token < 0) {
+        if (threadIdx.x == 0) {
+            if (out.logprob) out.logprob[r] = 0.0f;
+            if (out.entropy) out.entropy[r] = 0.0f;
+            if (out.stats) out.stats[2 * r] = out.stats[2 * r + 1] = 0.0f;
+        }
+        if ((int)threadIdx.x < out.top) {
+            ids[threadIdx.x] = -1;
+            lps[threadIdx.x] = 0.0f;
+        }
+        return;
+    }
+    const Running a = block_merge<THREADS>(row_running<T, THREADS, 4>(row, vocab, k), k, part);
+    const bool empty = a.m == -kInf && a.s == 0.0f;
+    const bool bad = !(a.s < kInf);  // a NaN or +infinity in the row
+    const float logsum = empty ? 0.0f : bad ? quiet_nan() : logf(a.s);
+    if (threadIdx.x == 0) {
+        if (out.logprob) {
+            float lp = quiet_nan();
+            if (token < vocab) lp = empty ? -kInf : (Vec<T>::one(row[token]) - a.m) * inv_t - logsum;
+            out.logprob[r] = lp;
+        }
+        if (out.entropy) out.entropy[r] = empty ? 0.0f : logsum - kLn2 * (a.t / a.s);
+        if (out.stats) {
+            out.stats[2 * r] = a.m;
+            out.stats[2 * r + 1] = logsum;
+        }
+    }
+    if (out.top == 0) return;
+    if (bad) {
+        if ((int)threadIdx.x < out.top) {
+            ids[threadIdx.x] = -1;
+            lps[threadIdx.x] = quiet_nan();
+        }
+        return;
+    }
+    top_by_rounds<T, THREADS>(row, vocab, out.top, a.m, inv_t, logsum, ids, lps, lx, li);
+}
+
+// ------------------------------------------------------------------ gradient of the log-probabilities
+
+constexpr int kGradThreads = 256;
+constexpr int kGradU = 4;  // vectors a thread handles
+
+template <typename T>
+__global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits, int64_t stride, int64_t vocab,
+                                                                unsigned tiles, float inv_t, float k,
+                                                                LogprobsGradIn in, T* grad, int64_t grad_stride) {
+    constexpr int N = Vec<T>::kN;
+    const int64_t r = blockIdx.x / tiles;
+    const int64_t tile = blockIdx.x % tiles;
+    const T* row = logits + r * stride;
+    T* g = grad + r * grad_stride;
+    const int64_t token = in.tokens[r];
+    const float m = in.stats[2 * r], logsum = in.stats[2 * r + 1];
+    const bool zero = token < 0 || m == -kInf;
+    const float gl = token >= vocab ? quiet_nan() : in.grad_logprob[r];
+    const float gh = in.grad_entropy ? in.grad_entropy[r] : 0.0f;
+    const float h = in.grad_entropy ? in.entropy[r] : 0.0f;
+    const int64_t nv = vocab / N;
+    // -(g_l + g_h (l + H)) p / T + [j == t] g_l / T
+    auto value = [&](float x, int64_t j) {
+        if (zero) return 0.0f;
+        const float d = x - m;
+        const float l = d * inv_t - logsum;
+        const float p = exp2f(d * k - logsum * (1.0f / kLn2));
+        const float hot = j == token ? gl : 0.0f;
+        return (hot - p * (gl + gh * (fmaxf(l, kLowest) + h))) * inv_t;
+    };
+    const int64_t v0 = tile * (kGradThreads * kGradU) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kGradU; ++u) {
+        const int64_t v = v0 + u * kGradThreads;
+        if (v < nv) {
+            const u32x4 x = zero ? u32x4{0, 0, 0, 0} : load_vec(row + v * N);
+            float f[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = value(Vec<T>::get(x, i), v * N + i);
+            store_vec(g + v * N, Vec<T>::pack(f));
+        } else {
+            const int64_t j = nv * N + (v - nv);  // the tail's elements take the threads behind the last vector
+            if (j < vocab) g[j] = Vec<T>::round(value(zero ? 0.0f : Vec<T>::one(row[j]), j));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ distillation
+
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float* part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < THREADS / 64; ++w) v += part[w];
+    __syncthreads();
+    return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float block_max(float v, float* part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < THREADS / 64; ++w) v = fmaxf(v, part[w]);
+    __syncthreads();
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void fill_row(T* g, int64_t vocab, float f) {
+    for (int64_t j = threadIdx.x; j < vocab; j += blockDim.x) g[j] = Vec<T>::round(f);
+}
+
+// One block per row: the teacher's distribution into shared memory, the
+// student's running softmax, the loss, then the gradient in a second pass over
+// the row and the teacher's entries set right in it.
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t stride, int64_t vocab, Teacher te,
+                                                     float temperature, float inv_t, float k,
+                                                     float* __restrict__ loss, T* grad, int64_t grad_stride) {
+    constexpr int N = Vec<T>::kN;
+    __shared__ Running part[THREADS / 64];
+    __shared__ float fpart[THREADS / 64];
+    __shared__ float q[ZS_DISTILL_MAX_K];
+    __shared__ float xs[ZS_DISTILL_MAX_K];
+    __shared__ int32_t id[ZS_DISTILL_MAX_K];
+    const int64_t r = blockIdx.x;
+    const T* row = logits + r * stride;
+    T* g = grad + r * grad_stride;
+    const int32_t* ids = te.ids + r * te.k;
+    const float* tl = te.logits + r * te.k;
+    const float w = te.row_weight ? te.row_weight[r] : 1.0f;
+    // the teacher's largest logit; 0 x of it is NaN where one is NaN or +infinity
+    float tmax = -kInf, bad = 0.0f;
+    for (int i = threadIdx.x; i < te.k; i += THREADS) {
+        const int32_t j = ids[i];
+        id[i] = j;
+        if (j < 0) continue;
+        tmax = fmaxf(tmax, tl[i]);
+        if (j >= vocab || !(tl[i] < kInf)) bad = 1.0f;
+    }
+    tmax = block_max<THREADS>(tmax, fpart);
+    bad = block_max<THREADS>(bad, fpart);
+    if (w == 0.0f || (tmax == -kInf && bad == 0.0f)) {
+        if (threadIdx.x == 0) loss[r] = 0.0f;
+        if (grad) fill_row(g, vocab, 0.0f);
+        return;
+    }
+    if (bad != 0.0f) {
+        if (threadIdx.x == 0) loss[r] = quiet_nan();
+        if (grad) fill_row(g, vocab, quiet_nan());
+        return;
+    }
+    float qs = 0.0f;
+    for (int i = threadIdx.x; i < te.k; i += THREADS) {
+        const float e = id[i] < 0 ? 0.0f : exp2f((tl[i] - tmax) * k);
+        q[i] = e;
+        qs += e;
+    }
+    qs = block_sum<THREADS>(qs, fpart);
+    const float inv_qs = 1.0f / qs, logqs = logf(qs);
+    const Running a = block_merge<THREADS>(row_running<T, THREADS, 4>(row, vocab, k), k, part);
+    const float m = base_of(a.m);
+    const float logsum = logf(a.s), inv_s = a.s == 0.0f ? 0.0f : 1.0f / a.s;
+    // loss: log q - log p = (t - tmax) / T - (x - m) / T + (log s - log sum of q's)
+    float l = 0.0f;
+    for (int i = threadIdx.x; i < te.k; i += THREADS) {
+        const float qi = q[i] * inv_qs;
+        q[i] = qi;
+        if (!(qi > 0.0f)) continue;
+        const float x = Vec<T>::one(row[id[i]]);
+        xs[i] = x;
+        l += qi * (((tl[i] - tmax) - (x - m)) * inv_t + (logsum - logqs));
+    }
+    l = block_sum<THREADS>(l, fpart);
+    if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf ? kInf : l);
+    if (!grad) return;
+    const float scale = w * temperature;
+    const float c = scale * inv_s;
+    const int64_t nv = vocab / N;
+    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
+        const u32x4 x = load_vec(row + v * N);
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = c * exp2f((Vec<T>::get(x, i) - m) * k);
+        store_vec(g + v * N, Vec<T>::pack(f));
+    }
+    const int64_t tail = nv * N + threadIdx.x;
+    if (tail < vocab) g[tail] = Vec<T>::round(c * exp2f((Vec<T>::one(row[tail]) - m) * k));
+    // the entries' tokens: written again with the teacher's share, once for
+    // each token by the first of its entries
+    __syncthreads();
+    for (int i = threadIdx.x; i < te.k; i += THREADS) {
+        if (!(q[i] > 0.0f)) continue;
+        bool first = true;
+        for (int j = 0; j < i; ++j)
+            if (id[j] == id[i] && q[j] > 0.0f) first = false;
+        if (!first) continue;
+        float qi = q[i];
+        for (int j = i + 1; j < te.k; ++j)
+            if (id[j] == id[i]) qi += q[j];
+        g[id[i]] = Vec<T>::round(c * exp2f((xs[i] - m) * k) - scale * qi);
+    }
+}
+
+}  // namespace
+
+int launch_logprobs(Rows logits, int dtype, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
+                    const LogprobsOut& out, void* stream) {
+    const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == ZS_DTYPE_BF16)
+        hipLaunchKernelGGL((k_logprobs<uint16_t, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
+                           static_cast<const uint16_t*>(logits.p), logits.stride, vocab, tokens, inv_t, k, out);
+    else
+        hipLaunchKernelGGL((k_logprobs<float, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
+                           static_cast<const float*>(logits.p), logits.stride, vocab, tokens, inv_t, k, out);
+    return (int)hipGetLastError();
+}
+
+namespace {
+
+template <typename T>
+int run_grad(Rows logits, int64_t rows, int64_t vocab, double temperature, const LogprobsGradIn& in, void* grad,
+             int64_t grad_stride, hipStream_t s) {
+    constexpr int N = Vec<T>::kN;
+    // the row's vectors, and one thread for each element of its tail
+    const int64_t per = kGradThreads * kGradU;
+    const int64_t tiles = (vocab / N + vocab % N + per - 1) / per;
+    if (rows * tiles > ((int64_t(1) << 32) - 1) / kGradThreads) return (int)hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_logprobs_grad<T>), dim3((unsigned)(rows * tiles)), dim3(kGradThreads), 0, s,
+                       static_cast<const T*>(logits.p), logits.stride, vocab, (unsigned)tiles,
+                       (float)(1.0 / temperature), (float)(M_LOG2E / temperature), in, static_cast<T*>(grad),
+                       grad_stride);
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_logprobs_grad(Rows logits, int dtype, int64_t rows, int64_t vocab, double temperature,
+                         const LogprobsGradIn& in, void* grad, int64_t grad_stride, void* stream) {
+    if (dtype == ZS_DTYPE_BF16)
+        return run_grad<uint16_t>(logits, rows, vocab, temperature, in, grad, grad_stride, (hipStream_t)stream);
+    return run_grad<float>(logits, rows, vocab, temperature, in, grad, grad_stride, (hipStream_t)stream);
+}
+
+int launch_distill(Rows logits, int dtype, int64_t rows, int64_t vocab, const Teacher& t, double temperature,
+                   float* loss, void* grad, int64_t grad_stride, void* stream) {
+    const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == ZS_DTYPE_BF16)
+        hipLaunchKernelGGL((k_distill<uint16_t, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
+                           static_cast<const uint16_t*>(logits.p), logits.stride, vocab, t, (float)temperature, inv_t,
+                           k, loss, static_cast<uint16_t*>(grad), grad_stride);
+    else
+        hipLaunchKernelGGL((k_distill<float, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
+                           static_cast<const float*>(logits.p), logits.stride, vocab, t, (float)temperature, inv_t, k,
+                           loss, static_cast<float*>(grad), grad_stride);
+    return (int)hipGetLastError();
+}
+
+}  // namespace zs
