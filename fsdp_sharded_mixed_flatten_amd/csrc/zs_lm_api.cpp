@@ -12,6 +12,10 @@ constexpr int64_t kMaxVocab = int64_t(1) << 30;
 // Rows of one call: a launch covers at most 2^32 - 1 work-items and a row
 // takes up to 1024 of them.
 constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;
+// Largest weight matrix: a wave (64 work-items) a row in one launch, columns
+// counted in int32.
+constexpr int64_t kMaxOut = int64_t(1) << 25;
+constexpr int64_t kMaxIn = int64_t(1) << 30;
 // Largest row stride and matrix extent: byte addresses stay far inside int64.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
@@ -105,9 +109,9 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
     if (tensor < 0 || tensor >= (int32_t)plan->tensors.size())
         return report(ZS_EINVAL, "tensor %d is not one of the plan's %d", tensor, (int)plan->tensors.size());
     const zs::TensorEntry& t = plan->tensors[(size_t)tensor];
-    if (out_features < 0 || in_features < 0 || out_features > (int64_t(1) << 31) - 1 ||
-        in_features > (int64_t(1) << 31) - 1 || out_features * in_features != t.numel)
-        return report(ZS_EINVAL, "tensor %d has %lld elements, not %lld x %lld (each below 2^31)", tensor,
+    if (out_features < 0 || in_features < 0 || out_features > kMaxOut || in_features > kMaxIn ||
+        out_features * in_features != t.numel)
+        return report(ZS_EINVAL, "tensor %d has %lld elements, not %lld x %lld (at most 2^25 x 2^30)", tensor,
                       (long long)t.numel, (long long)out_features, (long long)in_features);
     if (rows < 0 || rows > ZS_QUANT_MATVEC_MAX_ROWS)
         return report(ZS_EINVAL, "rows = %d outside [0, %d]", rows, ZS_QUANT_MATVEC_MAX_ROWS);

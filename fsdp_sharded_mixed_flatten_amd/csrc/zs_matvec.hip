@@ -133,13 +133,15 @@ void run_any(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64
 // bits) or 32 bytes (8 bits) at an aligned address, and scale i of the payload
 // belongs to elements [i * block, (i + 1) * block).
 //
-// A wave takes 16 * RT rows of W and, of every row, 128 columns at a time
-// (a chunk): lane (g, r) = (lane / 16, lane % 16) loads the 32 codes of row r
-// in columns 32 g ... 32 g + 31. Codes become bf16 (exact: they have at most
-// 8 significant bits) and multiply x in v_mfma_f32_16x16x32_bf16 with x as the
+// A wave takes 16 rows of W and, of every row, 128 columns at a time (a
+// chunk): lane (g, r) = (lane / 16, lane % 16) loads the 32 codes of row r in
+// columns 32 g ... 32 g + 31. Codes become bf16 (exact: they have at most 8
+// significant bits) and multiply x in v_mfma_f32_16x16x32_bf16 with x as the
 // first operand (its 16 rows are rows of x) and W as the second (its 16
 // columns are rows of W), so the scale, one a row of W, is one a lane of the
-// result and is applied in fp32 to sums over whole blocks.
+// result and is applied in fp32 to sums over whole blocks. Against fp32
+// multiply-adds this leaves 1.6 vector instructions a weight instead of more
+// than 3 and about none a row of x.
 //
 // One such instruction sums 32 columns, 8 from each group of 16 lanes. With
 // blocks of 128 or more the order of the columns inside a chunk is free, and
@@ -147,15 +149,19 @@ void run_any(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64
 // a chunk) it has to take the four groups' words from one block: the 4 x 4
 // words are transposed between the groups of lanes, one exchange a word.
 //
-// The waves of a workgroup share its rows and take turns over the chunks;
-// their sums meet in shared memory. No partial sum leaves the workgroup.
+// Row i * 4 + g of 16 rows of x is register i of lane group g in the result,
+// so that up to 4 rows take one register. Lanes without a row of x repeat
+// another's: their rows of the result are not stored.
 //
-// 16 rows of x fill the instruction; with fewer, the unused rows repeat one and
-// the rows are spread over the lane groups so that the result's first NI
-// registers hold them all (row i * 4 + g of x is register i of group g).
+// A wave loads spans of SPAN chunks at once (codes, the span's scales as
+// 16-byte loads) and the next span's before it computes a span. Plain loads:
+// a row's 64 bytes of a chunk are half a cache line, and with the nontemporal
+// hint the line's other half came from memory again (28672 x 8192 int4, one
+// row of x: 31.6 against 24.5 us).
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 __attribute__((aligned(4))) f32x4_u4;
 
 constexpr int kChunk = 128;
 
@@ -166,7 +172,7 @@ struct Codes<4> {
     u32x4 w;
     __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
     __device__ __forceinline__ void load(const char* p) {
-        w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+        w = *reinterpret_cast<const u32x4*>(p);
     }
     __device__ __forceinline__ void transpose() {
         auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
@@ -196,8 +202,8 @@ struct Codes<8> {
     u32x4 w[2];
     __device__ __forceinline__ void zero() { w[0] = w[1] = u32x4{0, 0, 0, 0}; }
     __device__ __forceinline__ void load(const char* p) {
-        w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-        w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + 1);
+        w[0] = *reinterpret_cast<const u32x4*>(p);
+        w[1] = reinterpret_cast<const u32x4*>(p)[1];
     }
     __device__ __forceinline__ void transpose() {
         // word j is the pair (w[j / 2][2 (j % 2)], w[j / 2][2 (j % 2) + 1])
@@ -226,188 +232,384 @@ struct Codes<8> {
     }
 };
 
-// NB: blocks a chunk (1: blocks of 128 or 256). MT: 16-row tiles of x. NI: of a
-// tile's 4 result registers, those that hold rows of x. RT: 16-row tiles of W
-// a wave. SPAN: chunks a wave loads together.
-template <int BITS, int NB, int MT, int NI, int RT, int SPAN>
-__global__ __launch_bounds__(512) void k_matvec_block(QuantWeight w, const uint16_t* __restrict__ x, int64_t x_stride,
-                                                      int rows, void* __restrict__ y, int y_bf16, int64_t y_stride) {
-    extern __shared__ float sums[];  // [waves - 1][RT * MT * NI][64]
+// What a wave loads of W for one span.
+template <int BITS, int SHIFT, int SPAN>
+struct Span {
+    static constexpr int NB = SHIFT >= 7 ? 1 : kChunk >> SHIFT;  // blocks a chunk (1: a block is a chunk or two)
+    static constexpr int kScales = SPAN * kChunk >= 1 << SHIFT ? SPAN * kChunk >> SHIFT : 1;
+    Codes<BITS> c[SPAN];
+    float s[kScales];
+
+    // The span of columns from k0. TAIL: it may reach past the row's end, where
+    // codes and scales count as zero.
+    template <bool TAIL>
+    __device__ __forceinline__ void load(const char* code, const float* scale, int k0, int n_in, int g) {
+#pragma unroll
+        for (int p = 0; p < SPAN; ++p) {
+            const int k = k0 + p * kChunk;
+            if (!TAIL || k + 32 * g < n_in)
+                c[p].load(code + (int64_t)k * BITS / 8);
+            else
+                c[p].zero();
+        }
+        const float* sp = scale + (k0 >> SHIFT);
+        if (TAIL) {
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) s[i] = k0 + (i << SHIFT) < n_in ? sp[i] : 0.0f;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kScales; i += 4) {
+            if (kScales - i >= 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4_u4*>(sp + i);
+                s[i] = v[0], s[i + 1] = v[1], s[i + 2] = v[2], s[i + 3] = v[3];
+            } else {
+#pragma unroll
+                for (int n = i; n < kScales; ++n) s[n] = sp[n];
+            }
+        }
+    }
+
+    // acc += scales * (chunk p of W times x): xv[m][j] is the lane's operand for
+    // instruction j of tile m of x.
+    template <int MT, int NI>
+    __device__ __forceinline__ void multiply(int p, const u32x4 (&xv)[MT][4], f32x4 (&acc)[MT]) {
+        if (NB > 1) c[p].transpose();
+        f32x4 part[MT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bf16x8 cv = c[p].word(j);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[m][j]), cv,
+                                                                  j % (4 / NB) == 0 ? zero : part[m], 0, 0, 0);
+            }
+            if ((j + 1) % (4 / NB) == 0) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        acc[m][i] = __builtin_fmaf(part[m][i], s[(p * kChunk + j * 32) >> SHIFT], acc[m][i]);
+            }
+        }
+    }
+    // Columns of a chunk between a lane's operands for instructions j and j + 1,
+    // and between lane groups, in units of 8.
+    static constexpr int kUnitJ = NB == 1 ? 1 : 4, kUnitG = NB == 1 ? 4 : 1;
+};
+
+// The codes and scales of the row of W that this lane loads, from its column
+// 32 g on. Rows behind the last one repeat it and are not stored.
+template <int BITS, int SHIFT>
+__device__ __forceinline__ void row_of(const QuantWeight& w, int64_t o, int g, const char** code,
+                                       const float** scale) {
+    const int64_t j = w.off + (o < w.n_out ? o : w.n_out - 1) * w.n_in;
+    *code = static_cast<const char*>(w.codes) + (j + 32 * g) * BITS / 8;
+    *scale = w.scales + (j >> SHIFT);
+}
+
+// Up to 4 rows of x, ROWS of them through shared memory: a wave loads its
+// span's columns of each row once, contiguously, and its lanes read their
+// operands from there (loading operands straight from x issues 4 wide loads a
+// chunk that mostly repeat each other, and took 36 instead of 24.5 us at 28672
+// x 8192 int4). The waves of a workgroup share its 16 rows of W and take turns
+// over the spans; their sums meet in shared memory at the end.
+// Reads at 5.1 TB/s at 28672 x 8192 int4 (24.5 us, one row), 6.0 TB/s at 8192 x
+// 128256 int8 (180 us, 4 rows); bound by memory there and by latency in
+// products of a few MB (4096 x 4096 int4 4.6 us, an empty launch 1.6 us).
+template <int BITS, int SHIFT, int SPAN, int ROWS>
+__global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_t* __restrict__ x, int64_t x_stride,
+                                                    int rows, void* __restrict__ y, int y_bf16, int64_t y_stride) {
+    using S = Span<BITS, SHIFT, SPAN>;
+    constexpr int kUnits = SPAN * kChunk / 8;  // 16-byte units of a row of x in a span: a lane each
+    constexpr int kPitch = kUnits + 4;
+    static_assert(kUnits <= 64, "a wave loads a row of x at once");
+    extern __shared__ u32x4 shared[];  // [waves][ROWS][kPitch], then the sums of waves 1 ... [waves - 1][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int g = lane >> 4, r = lane & 15;
-    const int64_t o0 = (int64_t)blockIdx.x * (16 * RT);
+    const int64_t o = (int64_t)blockIdx.x * 16 + r;
     const int n_in = (int)w.n_in;
-
-    const char* code[RT];
-    const float* scale[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        int64_t o = o0 + 16 * t + r;
-        if (o >= w.n_out) o = w.n_out - 1;  // rows behind the last one repeat it and are not stored
-        const int64_t j = w.off + o * w.n_in;
-        code[t] = static_cast<const char*>(w.codes) + (j + 32 * g) * BITS / 8;
-        scale[t] = w.scales + (j >> w.block_shift);
-    }
-    // the row of x this lane feeds, and its columns inside a chunk
+    const char* code;
+    const float* scale;
+    row_of<BITS, SHIFT>(w, o, g, &code, &scale);
+    u32x4* const xs = shared + wave * (ROWS * kPitch);
     const int token = (r & 3) * 4 + (r >> 2);
-    const uint16_t* xp[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        // lanes without a row of x repeat one: their row of the result is not stored
-        const int row = 16 * m + token < rows ? 16 * m + token : 0;
-        xp[m] = x + row * x_stride + (NB == 1 ? 32 : 8) * g;
-    }
+    const u32x4* const xr = xs + (token < rows ? token : 0) * kPitch + S::kUnitG * g;
 
-    f32x4 acc[RT][MT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // One span of columns from k0; TAIL: it reaches past the row's end, where
-    // codes, scales and x count as zero.
-    auto span = [&](int k0, auto tail) {
+    f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    struct Loaded {
+        S s;
+        u32x4 x[ROWS];
+    };
+    auto load = [&](Loaded& b, int k0, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
-        Codes<BITS> c[SPAN][RT];
-        float s[SPAN][RT][NB];
+        b.s.template load<TAIL>(code, scale, k0, n_in, g);
+        const int k = k0 + 8 * lane;
 #pragma unroll
-        for (int p = 0; p < SPAN; ++p) {
-            const int k = k0 + p * kChunk;
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                if (!TAIL || k + 32 * g < n_in)
-                    c[p][t].load(code[t] + (int64_t)k * BITS / 8);
-                else
-                    c[p][t].zero();
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int kb = k + b * (kChunk / NB);
-                    s[p][t][b] = !TAIL || kb < n_in ? scale[t][kb >> w.block_shift] : 0.0f;
-                }
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < SPAN; ++p) {
-            const int k = k0 + p * kChunk;
-            if (TAIL && k >= n_in) break;
-            bf16x8 xv[MT][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int kj = k + (NB == 1 ? 8 : 32) * j;  // this lane's columns: kj + (32 or 8) g ...
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    u32x4 v = u32x4{0, 0, 0, 0};
-                    if (!TAIL || kj + (NB == 1 ? 32 : 8) * g < n_in)
-                        v = *reinterpret_cast<const u32x4_u2*>(xp[m] + kj);
-                    xv[m][j] = __builtin_bit_cast(bf16x8, v);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                if (NB > 1) c[p][t].transpose();
-                f32x4 part[MT];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 cv = c[p][t].word(j);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                        part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m][j], cv,
-                                                                          j % (4 / NB) == 0 ? zero : part[m], 0, 0, 0);
-                    }
-                    if ((j + 1) % (4 / NB) == 0) {
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int i = 0; i < NI; ++i)
-                                acc[t][m][i] = __builtin_fmaf(part[m][i], s[p][t][j * NB / 4], acc[t][m][i]);
-                    }
-                }
-            }
+        for (int m = 0; m < ROWS; ++m) {
+            b.x[m] = u32x4{0, 0, 0, 0};
+            if (m < rows && lane < kUnits && (!TAIL || k < n_in))
+                b.x[m] = *reinterpret_cast<const u32x4_u2*>(x + m * x_stride + k);
         }
     };
-    int k0 = wave * (SPAN * kChunk);
-    for (; k0 + SPAN * kChunk <= n_in; k0 += waves * (SPAN * kChunk)) span(k0, std::false_type{});
-    if (k0 < n_in) span(k0, std::true_type{});
-
-    // the waves' sums, in the order of the waves
-    if (wave > 0) {
+    auto compute = [&](Loaded& b, int k0, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        // written and read by this wave's lanes only: in order, no barrier
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int m = 0; m < ROWS; ++m)
+            if (lane < kUnits) xs[m * kPitch + lane] = b.x[m];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u32x4 xv[SPAN][1][4];
+#pragma unroll
+        for (int p = 0; p < SPAN; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xv[p][0][j] = xr[p * (kChunk / 8) + S::kUnitJ * j];
+#pragma unroll
+        for (int p = 0; p < SPAN; ++p) {
+            if (TAIL && k0 + p * kChunk >= n_in) break;
+            b.s.template multiply<1, 1>(p, xv[p], acc);
+        }
+    };
+    // whole spans, then the row's last one if it is none
+    constexpr int kSpan = SPAN * kChunk;
+    const int step = waves * kSpan;
+    int k0 = wave * kSpan;
+    if (k0 + kSpan <= n_in) {
+        Loaded a, b;
+        load(a, k0, std::false_type{});
+        while (true) {
+            const bool more = k0 + step + kSpan <= n_in;
+            if (more) load(b, k0 + step, std::false_type{});
+            compute(a, k0, std::false_type{});
+            k0 += step;
+            if (!more) break;
+            const bool again = k0 + step + kSpan <= n_in;
+            if (again) load(a, k0 + step, std::false_type{});
+            compute(b, k0, std::false_type{});
+            k0 += step;
+            if (!again) break;
+        }
+    }
+    if (k0 < n_in) {
+        Loaded a;
+        load(a, k0, std::true_type{});
+        compute(a, k0, std::true_type{});
+    }
+    // the waves' sums, in the order of the waves
+    float* const sums = reinterpret_cast<float*>(shared + waves * (ROWS * kPitch));
+    if (wave > 0) sums[(wave - 1) * 64 + lane] = acc[0][0];
+    __syncthreads();
+    if (wave > 0) return;
+    float v = acc[0][0];
+    for (int q = 1; q < waves; ++q) v += sums[(q - 1) * 64 + lane];
+    if (g < rows && o < w.n_out) store_y(y, y_bf16, g * y_stride + o, v * Codes<BITS>::kUnit);
+}
+
+// 5 and more rows of x, in MT tiles of 16: what costs here is bringing x to the
+// waves (each needs all of it), so RW waves with 16 rows of W each share a
+// span of x in shared memory, and KW such groups take turns over the spans.
+// One barrier a turn; x of the next turn is loaded beside its codes and goes
+// into the other half of the buffer.
+// 28672 x 8192 int4 with 16 rows: 44 us against 76 with each wave loading its
+// own operands, 64 rows 118 against 258; at 2048 x 11008 with 16 rows 9.2
+// against 10.8.
+template <int BITS, int SHIFT, int MT, int SPAN, int RW, int KW>
+__global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, const uint16_t* __restrict__ x,
+                                                              int64_t x_stride, int rows, void* __restrict__ y,
+                                                              int y_bf16, int64_t y_stride) {
+    using S = Span<BITS, SHIFT, SPAN>;
+    constexpr int kSpan = SPAN * kChunk;
+    constexpr int kUnits = kSpan / 8;           // 16-byte units of a row of x in a span
+    constexpr int kPitch = kUnits + 1;          // rows start in different banks
+    constexpr int kTile = 16 * MT * kPitch;     // one group's x
+    constexpr int kLoads = 16 * MT * kUnits / (64 * RW);
+    static_assert(kLoads * 64 * RW == 16 * MT * kUnits, "a group loads whole spans of x");
+    constexpr int kX = 2 * KW * kTile * 16, kS = (KW - 1) * RW * MT * 4 * 64 * 4;
+    __shared__ __attribute__((aligned(16))) char shared[kX > kS ? kX : kS];
+    u32x4* const xl = reinterpret_cast<u32x4*>(shared);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rw = wave % RW, kw = wave / RW;
+    const int g = lane >> 4, r = lane & 15;
+    const int64_t o = ((int64_t)blockIdx.x * RW + rw) * 16 + r;
+    const int n_in = (int)w.n_in;
+    const int turns = (n_in + KW * kSpan - 1) / (KW * kSpan);
+    const char* code;
+    const float* scale;
+    row_of<BITS, SHIFT>(w, o, g, &code, &scale);
+    const int token = (r & 3) * 4 + (r >> 2);
+    int xrow[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xrow[m] = (16 * m + token < rows ? 16 * m + token : 0) * kPitch + S::kUnitG * g;
+
+    f32x4 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 xn[kLoads];
+    auto load = [&](S& b, int turn) {
+        const int k0 = (turn * KW + kw) * kSpan;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = rw * 64 + lane + i * (64 * RW), row = u / kUnits, k = k0 + u % kUnits * 8;
+            xn[i] = u32x4{0, 0, 0, 0};
+            if (row < rows && k < n_in) xn[i] = *reinterpret_cast<const u32x4_u2*>(x + row * x_stride + k);
+        }
+        if (k0 + kSpan <= n_in)
+            b.template load<false>(code, scale, k0, n_in, g);
+        else
+            b.template load<true>(code, scale, k0, n_in, g);
+    };
+    auto store = [&](int turn) {
+        u32x4* to = xl + ((turn & 1) * KW + kw) * kTile;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = rw * 64 + lane + i * (64 * RW);
+            to[u / kUnits * kPitch + u % kUnits] = xn[i];
+        }
+    };
+    auto compute = [&](S& b, int turn) {
+        const u32x4* from = xl + ((turn & 1) * KW + kw) * kTile;
+#pragma unroll
+        for (int p = 0; p < SPAN; ++p) {
+            u32x4 xv[MT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) xv[m][j] = from[xrow[m] + p * (kChunk / 8) + S::kUnitJ * j];
+            b.template multiply<MT, 4>(p, xv, acc);
+        }
+    };
+    S a, b;
+    load(a, 0);
+    store(0);
+    __syncthreads();
+    for (int turn = 0; turn < turns; turn += 2) {
+        if (turn + 1 < turns) load(b, turn + 1);
+        compute(a, turn);
+        if (turn + 1 >= turns) break;
+        store(turn + 1);
+        __syncthreads();
+        if (turn + 2 < turns) load(a, turn + 2);
+        compute(b, turn + 1);
+        if (turn + 2 < turns) store(turn + 2);
+        __syncthreads();
+    }
+    if (KW > 1) {  // the groups' sums, in the order of the groups
+        float* const sums = reinterpret_cast<float*>(shared);
+        __syncthreads();
+        if (kw > 0) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    sums[((wave - 1) * (RT * MT * NI) + (t * MT + m) * NI + i) * 64 + lane] = acc[t][m][i];
+                for (int i = 0; i < 4; ++i) sums[(((kw - 1) * RW + rw) * (MT * 4) + m * 4 + i) * 64 + lane] = acc[m][i];
+        }
+        __syncthreads();
+        if (kw > 0) return;
+#pragma unroll
+        for (int q = 1; q < KW; ++q)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][i] += sums[(((q - 1) * RW + rw) * (MT * 4) + m * 4 + i) * 64 + lane];
     }
-    __syncthreads();
-    if (wave > 0) return;
+    if (o >= w.n_out) return;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                float v = acc[t][m][i];
-                for (int q = 1; q < waves; ++q)
-                    v += sums[((q - 1) * (RT * MT * NI) + (t * MT + m) * NI + i) * 64 + lane];
-                const int row = 16 * m + 4 * i + g;
-                const int64_t o = o0 + 16 * t + r;
-                if (row < rows && o < w.n_out) store_y(y, y_bf16, row * y_stride + o, v * Codes<BITS>::kUnit);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int row = 16 * m + 4 * i + g;
+            if (row < rows) store_y(y, y_bf16, row * y_stride + o, acc[m][i] * Codes<BITS>::kUnit);
+        }
 }
 
-template <int BITS, int NB, int MT, int NI, int RT>
-void run_block_t(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64_t y_stride, hipStream_t s) {
-    constexpr int kSpan = RT * MT * BITS > 8 ? 2 : 4;
-    const int64_t spans = (w.n_in + kSpan * kChunk - 1) / (kSpan * kChunk);
-    const int waves = spans < 8 ? (int)spans : 8;
-    const size_t lds = (size_t)(waves - 1) * (RT * MT * NI) * 64 * sizeof(float);
-    hipLaunchKernelGGL((k_matvec_block<BITS, NB, MT, NI, RT, kSpan>),
-                       dim3((unsigned)((w.n_out + 16 * RT - 1) / (16 * RT))), dim3(64 * waves), lds, s, w,
-                       static_cast<const uint16_t*>(x.p), x.stride, rows, y, (int)y_bf16, y_stride);
+struct Product {
+    const QuantWeight& w;
+    Rows x;
+    int rows;
+    void* y;
+    int y_bf16;
+    int64_t y_stride;
+    hipStream_t s;
+};
+
+template <int BITS, int SHIFT, int ROWS>
+void run_few(const Product& a) {
+    constexpr int kSpanChunks = 4;
+    const int64_t tiles = (a.w.n_out + 15) / 16;
+    const int64_t spans = (a.w.n_in + kSpanChunks * kChunk - 1) / (kSpanChunks * kChunk);
+    // 8 waves a workgroup while a workgroup a CU is about all there is (4096 x
+    // 4096 int4 4.8 us against 5.4 with 4), else 4 (28672 x 8192 int4 24.4 us
+    // against 26.5 with 8, 8192 x 128256 114 against 147)
+    const int most = tiles <= 256 ? 8 : 4;
+    const int waves = spans < most ? (int)spans : most;
+    const size_t lds = (size_t)waves * ROWS * (kSpanChunks * kChunk / 8 + 4) * 16 + (size_t)(waves - 1) * 64 * 4;
+    hipLaunchKernelGGL((k_matvec_few<BITS, SHIFT, kSpanChunks, ROWS>), dim3((unsigned)tiles), dim3(64 * waves), lds,
+                       a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y, a.y_bf16, a.y_stride);
 }
 
-template <int BITS, int NB>
-void run_block_n(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64_t y_stride, hipStream_t s) {
-    if (rows <= 4)
-        run_block_t<BITS, NB, 1, 1, 1>(w, x, rows, y, y_bf16, y_stride, s);
-    else if (rows <= 8)
-        run_block_t<BITS, NB, 1, 2, 1>(w, x, rows, y, y_bf16, y_stride, s);
-    else if (rows <= 16)
-        run_block_t<BITS, NB, 1, 4, 1>(w, x, rows, y, y_bf16, y_stride, s);
-    else if (rows <= 32)
-        run_block_t<BITS, NB, 2, 4, 1>(w, x, rows, y, y_bf16, y_stride, s);
+template <int BITS, int SHIFT, int MT, int SPAN, int RW, int KW>
+void run_rows(const Product& a) {
+    hipLaunchKernelGGL((k_matvec_rows<BITS, SHIFT, MT, SPAN, RW, KW>),
+                       dim3((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW))), dim3(64 * RW * KW), 0, a.s, a.w,
+                       static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y, a.y_bf16, a.y_stride);
+}
+
+template <int BITS, int SHIFT>
+void run_block(const Product& a) {
+    // Where 128 rows of W a workgroup still fill the chip, all 8 waves share x
+    // (8192 x 128256 int4, 16 rows: 131 us against 192 with 4 groups of 4);
+    // elsewhere 2 do and 4 groups split the columns (28672 x 8192: 44 us
+    // against 68 with 2 groups of 4).
+    const bool wide = a.w.n_out >= 128 * 256;
+    if (a.rows == 1)
+        run_few<BITS, SHIFT, 1>(a);
+    else if (a.rows <= 4)
+        run_few<BITS, SHIFT, 4>(a);
+    else if (a.rows <= 16 && wide)
+        run_rows<BITS, SHIFT, 1, 4, 8, 1>(a);
+    else if (a.rows <= 16 && a.w.n_in > 2048)
+        run_rows<BITS, SHIFT, 1, 4, 2, 4>(a);
+    else if (a.rows <= 16)  // shorter spans where the long ones make one turn (2048 x 11008: 9.2 us against 11.6)
+        run_rows<BITS, SHIFT, 1, 2, 2, 4>(a);
+    else if (a.rows <= 32 && wide)
+        run_rows<BITS, SHIFT, 2, 2, 8, 1>(a);
+    else if (a.rows <= 32)
+        run_rows<BITS, SHIFT, 2, 2, 2, 4>(a);
+    else if (wide)
+        run_rows<BITS, SHIFT, 4, 1, 8, 1>(a);
     else
-        run_block_t<BITS, NB, 4, 4, 1>(w, x, rows, y, y_bf16, y_stride, s);
+        run_rows<BITS, SHIFT, 4, 1, 2, 4>(a);
 }
 
 template <int BITS>
-void run_block(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64_t y_stride, hipStream_t s) {
-    if (w.block_shift == 5)
-        run_block_n<BITS, 4>(w, x, rows, y, y_bf16, y_stride, s);
-    else if (w.block_shift == 6)
-        run_block_n<BITS, 2>(w, x, rows, y, y_bf16, y_stride, s);
-    else
-        run_block_n<BITS, 1>(w, x, rows, y, y_bf16, y_stride, s);
+void run_blocks(const Product& a) {
+    switch (a.w.block_shift) {
+        case 5: return run_block<BITS, 5>(a);
+        case 6: return run_block<BITS, 6>(a);
+        case 7: return run_block<BITS, 7>(a);
+        default: return run_block<BITS, 8>(a);
+    }
 }
 
 }  // namespace
 
 int launch_quant_matvec(const QuantWeight& w, Rows x, int rows, void* y, int y_dtype, int64_t y_stride,
                         void* stream) {
-    if (w.n_out > (int64_t)kAnyWaves * ((1 << 24) - 1)) return (int)hipErrorInvalidValue;  // 2^32 - 1 work-items
-    const bool y_bf16 = y_dtype == ZS_DTYPE_BF16;
+    const Product a{w, x, rows, y, y_dtype == ZS_DTYPE_BF16, y_stride, (hipStream_t)stream};
     const int64_t block = int64_t(1) << w.block_shift;
     const bool whole = block >= 32 && w.n_in > 0 && w.off % block == 0 && w.n_in % block == 0 && w.shard % block == 0;
     if (whole && w.bits == 4)
-        run_block<4>(w, x, rows, y, y_bf16, y_stride, (hipStream_t)stream);
+        run_blocks<4>(a);
     else if (whole)
-        run_block<8>(w, x, rows, y, y_bf16, y_stride, (hipStream_t)stream);
+        run_blocks<8>(a);
     else if (w.bits == 4)
-        run_any<4>(w, x, rows, y, y_bf16, y_stride, (hipStream_t)stream);
+        run_any<4>(w, x, rows, y, a.y_bf16, y_stride, a.s);
     else
-        run_any<8>(w, x, rows, y, y_bf16, y_stride, (hipStream_t)stream);
+        run_any<8>(w, x, rows, y, a.y_bf16, y_stride, a.s);
     return (int)hipGetLastError();
 }
 

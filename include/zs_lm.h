@@ -60,7 +60,7 @@ typedef enum zs_dtype { ZS_DTYPE_BF16 = 0, ZS_DTYPE_F32 = 1 } zs_dtype;
  * multiples of block and block >= 32, and slower elsewhere. A block whose
  * scale is NaN (an infinity or NaN among its parameters) gives NaN.
  *
- * FLAT plans. bits 4 or 8. x is bf16, y bf16 or fp32 (y_dtype).
+ * FLAT plans. bits 4 or 8. out_features <= 2^25, in_features <= 2^30. x is bf16, y bf16 or fp32 (y_dtype).
  * 0 <= rows <= ZS_QUANT_MATVEC_MAX_ROWS (more rows: dequantize once and use a
  * matrix product); rows == 0 or out_features == 0 does nothing, in_features
  * == 0 gives zeros. y may not overlap any input. */
