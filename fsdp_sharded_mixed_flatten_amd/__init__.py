@@ -247,6 +247,14 @@ class Plan:
 
     def __init__(self, handle):
         self._h = ctypes.c_void_p(handle)
+        self._shape = None
+
+    @property
+    def shape(self):
+        """(shard_numel, world_size), asked of the library once: a plan never changes."""
+        if self._shape is None:
+            self._shape = (self.shard_numel, self.world_size)
+        return self._shape
 
     @property
     def handle(self):
@@ -710,39 +718,56 @@ def zs_fused_shard_step_multi_dc(plan, coefs, n_groups, workspace, stream=None):
 
 
 # ---------------------------------------------------------------- language-model operators
+# A product for one token runs a few microseconds on the device, so what a call
+# does in Python is kept short: integers instead of torch's shape and device
+# objects, and error texts built only when a check fails.
+
+_torch = None
+
+
+def _lm_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _lm_device(t, what):
-    """The device of the call: that of its first tensor. The language-model
-    calls run on this device's current stream, whichever device is current."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+    """Index of the call's device, that of its first tensor. The
+    language-model calls run on this device's current stream, whichever device
+    is current."""
+    if not (isinstance(t, _lm_torch().Tensor) and t.is_cuda):
         raise ValueError(f"{what} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _lm_rows(t, dtypes, rows, cols, device, what):
-    """(address, row stride) of a [rows, cols] matrix whose rows are contiguous."""
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's first tensor on {device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _lm_elsewhere(t, device, what):
+    return ValueError(f"{what} is on {t.device}, the call's first tensor on cuda:{device}")
+
+
+def _lm_rows(t, rows, cols, device, what):
+    """Row stride of a [rows, cols] matrix whose rows are contiguous (its dtype is the caller's to check)."""
+    if t.get_device() != device:
+        raise _lm_elsewhere(t, device, what)
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
         raise ValueError(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{what} must have contiguous rows, its strides are {t.stride()}")
     # the stride of a single row is free, and may be anything in torch
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+    return t.stride(0) if rows > 1 else max(cols, 1)
 
 
-def _lm_array(t, dtype, shape, device, what):
-    """Address of a contiguous array of exactly this shape, or None."""
+def _lm_array(t, dtype, numel, cols, device, what):
+    """Address of a contiguous array of exactly [numel] (cols 0) or [numel / cols, cols], or None."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's first tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
+    if t.get_device() != device:
+        raise _lm_elsewhere(t, device, what)
+    if t.dtype is not dtype or t.numel() != numel or (t.dim() != 1 if cols == 0 else
+                                                      t.dim() != 2 or t.size(1) != cols):
+        shape = [numel] if cols == 0 else [numel // cols, cols]
+        raise ValueError(f"{what} must be {dtype} of shape {shape}, got {t.dtype} of {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
@@ -750,49 +775,68 @@ def _lm_array(t, dtype, shape, device, what):
 
 def _lm_call(fn, device, stream, *args):
     """Runs fn(*args, stream) with the call's device current."""
-    import torch
+    torch = _torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if not isinstance(stream, int):
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        if stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{device}")
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream))
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status != ZS_OK:
+        _check(status)
 
 
 def _lm_logits(logits):
-    """(device, dtype code, address, rows, vocab, row stride) of a [rows, vocab] matrix of logits."""
-    import torch
+    """(device, dtype code, rows, vocab, row stride) of a [rows, vocab] matrix of logits."""
     device = _lm_device(logits, "logits")
+    dtype = logits.dtype
+    if dtype is _torch.bfloat16:
+        code = ZS_DTYPE_BF16
+    elif dtype is _torch.float32:
+        code = ZS_DTYPE_F32
+    else:
+        raise ValueError(f"logits must be bfloat16 or float32, got {dtype}")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, vocab], got {list(logits.shape)}")
-    rows, vocab = logits.shape
-    ptr, stride = _lm_rows(logits, (torch.bfloat16, torch.float32), rows, vocab, device, "logits")
-    return device, ZS_DTYPE_BF16 if logits.dtype == torch.bfloat16 else ZS_DTYPE_F32, ptr, rows, vocab, stride
+    rows, vocab = logits.size(0), logits.size(1)
+    return device, code, rows, vocab, _lm_rows(logits, rows, vocab, device, "logits")
+
+
+def _lm_grad(grad, logits, rows, vocab, device):
+    if grad.dtype is not logits.dtype:
+        raise ValueError(f"grad_logits must be {logits.dtype} like the logits, got {grad.dtype}")
+    return grad.data_ptr(), _lm_rows(grad, rows, vocab, device, "grad_logits")
 
 
 def zs_quant_matvec(plan, tensor, out_features, in_features, bits, block, codes_all, scales_all, x, y, stream=None):
     """y[r, o] = sum_i W[o, i] x[r, i] with W = tensor `tensor` of the plan (out_features x in_features) read from
     the quantized gather's payload. x: bfloat16 [rows, in_features]; y: bfloat16 or float32 [rows, out_features]."""
-    import torch
     device = _lm_device(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [rows, {in_features}], got {list(x.shape)}")
-    rows = x.shape[0]
-    xp, xs = _lm_rows(x, (torch.bfloat16,), rows, in_features, device, "x")
-    yp, ys = _lm_rows(y, (torch.bfloat16, torch.float32), rows, out_features, device, "y")
-    S, N = plan.shard_numel, plan.world_size
-    for t, what in ((codes_all, "codes_all"), (scales_all, "scales_all")):
-        if not isinstance(t, int) and t.device != device:
-            raise ValueError(f"{what} is on {t.device}, x on {device}")
+    if x.dim() != 2 or x.dtype is not _torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 [rows, {in_features}], got {x.dtype} of {list(x.shape)}")
+    rows = x.size(0)
+    xs = _lm_rows(x, rows, in_features, device, "x")
+    ys = _lm_rows(y, rows, out_features, device, "y")
+    if y.dtype is _torch.bfloat16:
+        y_dtype = ZS_DTYPE_BF16
+    elif y.dtype is _torch.float32:
+        y_dtype = ZS_DTYPE_F32
+    else:
+        raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
+    S, N = plan.shape
+    if not isinstance(codes_all, int) and codes_all.get_device() != device:
+        raise _lm_elsewhere(codes_all, device, "codes_all")
+    if not isinstance(scales_all, int) and scales_all.get_device() != device:
+        raise _lm_elsewhere(scales_all, device, "scales_all")
     _lm_call(_lib.zs_quant_matvec, device, stream, plan.handle, tensor, out_features, in_features, bits, block,
              _ptr(codes_all, "bytes", N * S * bits // 8, "codes_all"),
-             _ptr(scales_all, "f32", N * -(-S // max(block, 1)), "scales_all"), xp, xs, rows, yp,
-             ZS_DTYPE_BF16 if y.dtype == torch.bfloat16 else ZS_DTYPE_F32, ys)
+             _ptr(scales_all, "f32", N * -(-S // max(block, 1)), "scales_all"), x.data_ptr(), xs, rows, y.data_ptr(),
+             y_dtype, ys)
 
 
 def zs_token_logprobs(logits, tokens, temperature=1.0, logprob=None, entropy=None, stats=None, top_ids=None,
@@ -800,39 +844,39 @@ def zs_token_logprobs(logits, tokens, temperature=1.0, logprob=None, entropy=Non
     """logits: bfloat16 or float32 [rows, vocab]; tokens: int32 [rows]. Outputs, each optional: logprob and entropy
     float32 [rows]; stats float32 [rows, 2], which the gradient takes; top_ids int32 and top_logprobs float32
     [rows, top], together."""
-    import torch
-    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
+    device, dtype, rows, vocab, stride = _lm_logits(logits)
+    i32, f32 = _torch.int32, _torch.float32
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs are given together")
     top = 0
     if top_ids is not None:
         if top_ids.dim() != 2:
             raise ValueError(f"top_ids must be [{rows}, top], got {list(top_ids.shape)}")
-        top = top_ids.shape[1]
-    if top == 0:
-        top_ids = top_logprobs = None
-    _lm_call(_lib.zs_token_logprobs, device, stream, ptr, dtype, rows, vocab, stride,
-             _lm_array(tokens, torch.int32, (rows,), device, "tokens"), temperature,
-             _lm_array(logprob, torch.float32, (rows,), device, "logprob"),
-             _lm_array(entropy, torch.float32, (rows,), device, "entropy"),
-             _lm_array(stats, torch.float32, (rows, 2), device, "stats"), top,
-             _lm_array(top_ids, torch.int32, (rows, top), device, "top_ids"),
-             _lm_array(top_logprobs, torch.float32, (rows, top), device, "top_logprobs"))
+        top = top_ids.size(1)
+        if top == 0:
+            top_ids = top_logprobs = None
+    _lm_call(_lib.zs_token_logprobs, device, stream, logits.data_ptr(), dtype, rows, vocab, stride,
+             _lm_array(tokens, i32, rows, 0, device, "tokens"), temperature,
+             _lm_array(logprob, f32, rows, 0, device, "logprob"),
+             _lm_array(entropy, f32, rows, 0, device, "entropy"),
+             _lm_array(stats, f32, 2 * rows, 2, device, "stats"), top,
+             _lm_array(top_ids, i32, rows * top, top, device, "top_ids"),
+             _lm_array(top_logprobs, f32, rows * top, top, device, "top_logprobs"))
 
 
 def zs_token_logprobs_backward(logits, tokens, stats, grad_logprob, grad_logits, temperature=1.0, entropy=None,
                                grad_entropy=None, stream=None):
     """grad_logits (the logits' dtype; logits itself for in place) from the forward call's stats and the gradients of
     logprob and, with the forward call's entropy, of entropy."""
-    import torch
-    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
-    gp, gs = _lm_rows(grad_logits, (logits.dtype,), rows, vocab, device, "grad_logits")
-    _lm_call(_lib.zs_token_logprobs_backward, device, stream, ptr, dtype, rows, vocab, stride,
-             _lm_array(tokens, torch.int32, (rows,), device, "tokens"), temperature,
-             _lm_array(stats, torch.float32, (rows, 2), device, "stats"),
-             _lm_array(entropy, torch.float32, (rows,), device, "entropy"),
-             _lm_array(grad_logprob, torch.float32, (rows,), device, "grad_logprob"),
-             _lm_array(grad_entropy, torch.float32, (rows,), device, "grad_entropy"), gp, gs)
+    device, dtype, rows, vocab, stride = _lm_logits(logits)
+    f32 = _torch.float32
+    gp, gs = _lm_grad(grad_logits, logits, rows, vocab, device)
+    _lm_call(_lib.zs_token_logprobs_backward, device, stream, logits.data_ptr(), dtype, rows, vocab, stride,
+             _lm_array(tokens, _torch.int32, rows, 0, device, "tokens"), temperature,
+             _lm_array(stats, f32, 2 * rows, 2, device, "stats"),
+             _lm_array(entropy, f32, rows, 0, device, "entropy"),
+             _lm_array(grad_logprob, f32, rows, 0, device, "grad_logprob"),
+             _lm_array(grad_entropy, f32, rows, 0, device, "grad_entropy"), gp, gs)
 
 
 def zs_distill_topk(logits, teacher_ids, teacher_logits, loss, grad_logits=None, temperature=1.0, row_weight=None,
@@ -840,19 +884,17 @@ def zs_distill_topk(logits, teacher_ids, teacher_logits, loss, grad_logits=None,
     """Distillation loss [rows] (float32) from the teacher's top entries (teacher_ids int32, teacher_logits float32,
     both [rows, k]; a negative id is unused) and, if given, its gradient grad_logits (the logits' dtype; logits itself
     for in place)."""
-    import torch
-    device, dtype, ptr, rows, vocab, stride = _lm_logits(logits)
+    device, dtype, rows, vocab, stride = _lm_logits(logits)
+    f32 = _torch.float32
     if teacher_ids.dim() != 2:
         raise ValueError(f"teacher_ids must be [{rows}, k], got {list(teacher_ids.shape)}")
-    k = teacher_ids.shape[1]
-    gp, gs = None, vocab
-    if grad_logits is not None:
-        gp, gs = _lm_rows(grad_logits, (logits.dtype,), rows, vocab, device, "grad_logits")
-    _lm_call(_lib.zs_distill_topk, device, stream, ptr, dtype, rows, vocab, stride,
-             _lm_array(teacher_ids, torch.int32, (rows, k), device, "teacher_ids"),
-             _lm_array(teacher_logits, torch.float32, (rows, k), device, "teacher_logits"), k, temperature,
-             _lm_array(row_weight, torch.float32, (rows,), device, "row_weight"),
-             _lm_array(loss, torch.float32, (rows,), device, "loss"), gp, gs)
+    k = teacher_ids.size(1)
+    gp, gs = (None, vocab) if grad_logits is None else _lm_grad(grad_logits, logits, rows, vocab, device)
+    _lm_call(_lib.zs_distill_topk, device, stream, logits.data_ptr(), dtype, rows, vocab, stride,
+             _lm_array(teacher_ids, _torch.int32, rows * k, k, device, "teacher_ids"),
+             _lm_array(teacher_logits, f32, rows * k, k, device, "teacher_logits"), k, temperature,
+             _lm_array(row_weight, f32, rows, 0, device, "row_weight"),
+             _lm_array(loss, f32, rows, 0, device, "loss"), gp, gs)
 
 
 def zs_last_error():
