@@ -55,7 +55,7 @@ struct Vec<uint16_t> {
         for (int i = 0; i < 4; ++i) v[i] = f32_bf16(f[2 * i]) | (f32_bf16(f[2 * i + 1]) << 16);
         return v;
     }
-    static constexpr uint32_t kNegInf = 0xFF80FF80u;
+    static constexpr uint32_t kNegInf = 0xFF80FF80u, kNan = 0x7FC07FC0u;
 };
 template <>
 struct Vec<float> {
@@ -66,7 +66,7 @@ struct Vec<float> {
     static __device__ __forceinline__ u32x4 pack(const float* f) {
         return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
     }
-    static constexpr uint32_t kNegInf = 0xFF800000u;
+    static constexpr uint32_t kNegInf = 0xFF800000u, kNan = 0x7FC00000u;
 };
 
 template <typename T>
@@ -132,44 +132,191 @@ __device__ __forceinline__ Running block_merge(Running r, float k, Running* part
 }
 
 // One thread's share of a row: vectors tid, tid + THREADS, ... and one element
-// of the tail behind the last whole vector.
-template <typename T, int THREADS, int U>
-__device__ __forceinline__ Running row_running(const T* __restrict__ row, int64_t vocab, float k) {
+// of the tail behind the last whole vector. Right for any logits.
+template <typename T, int THREADS>
+__device__ __forceinline__ Running row_running(const T* row, int64_t vocab, float k) {
     constexpr int N = Vec<T>::kN;
     const int64_t nv = vocab / N;
     Running r{-kInf, 0.0f, 0.0f};
-    for (int64_t v0 = threadIdx.x; v0 < nv; v0 += (int64_t)THREADS * U) {
-        u32x4 x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t v = v0 + (int64_t)u * THREADS;
-            const uint32_t none = Vec<T>::kNegInf;
-            x[u] = v < nv ? load_vec(row + v * N) : u32x4{none, none, none, none};
-        }
+    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
+        const u32x4 x = load_vec(row + v * N);
         float m = r.m;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < N; ++i) m = fmaxf(m, Vec<T>::get(x[u], i));
+        for (int i = 0; i < N; ++i) m = fmaxf(m, Vec<T>::get(x, i));
         rebase(r, m, k);
         const float b = base_of(m);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float s = 0.0f, t = 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float d = (Vec<T>::get(x[u], i) - b) * k;
-                const float e = exp2f(d);
-                s += e;
-                t += e * fmaxf(d, kLowest);
-            }
-            r.s += s;
-            r.t += t;
+        for (int i = 0; i < N; ++i) {
+            const float d = (Vec<T>::get(x, i) - b) * k;
+            const float e = exp2f(d);
+            r.s += e;
+            r.t += e * fmaxf(d, kLowest);
         }
     }
     const int64_t tail = nv * N + threadIdx.x;
     if (tail < vocab) add_one(r, Vec<T>::one(row[tail]), k);
     return r;
+}
+
+// ------------------------------------------------------------------ running softmax, ordinary logits
+// The same sums with one multiply-add a difference: relative to c, the rounded
+// product of the maximum and k, d = x k - c is off by one rounding of d itself
+// (that c is no exact multiple of k shifts every d alike). ENTROPY: t is kept.
+// Products past fp32's range, infinities, NaN and maxima so large that the
+// shift matters leave s 0, infinite or NaN, or are seen from the maximum
+// (ordinary() is false): the row is then summed by row_running.
+struct Fast {
+    float m, c, s, t;
+};
+
+__device__ __forceinline__ float exp2_raw(float d) { return __builtin_amdgcn_exp2f(d); }
+
+template <bool ENTROPY>
+__device__ __forceinline__ void fast_rebase(Fast& r, float m, float k) {
+    const float c = base_of(m) * k;
+    const float d = r.m == -kInf ? 0.0f : r.c - c;  // nothing seen yet: s = t = 0
+    const float f = exp2_raw(d);
+    if (ENTROPY) r.t = f * (r.t + r.s * fmaxf(d, kLowest));
+    r.s = f * r.s;
+    r.m = m;
+    r.c = c;
+}
+
+template <bool ENTROPY>
+__device__ __forceinline__ Fast fast_merge(Fast a, Fast b, float k) {
+    const float m = fmaxf(a.m, b.m);
+    fast_rebase<ENTROPY>(a, m, k);
+    fast_rebase<ENTROPY>(b, m, k);
+    return Fast{a.m, a.c, a.s + b.s, a.t + b.t};
+}
+
+template <typename T, bool ENTROPY, int U>
+__device__ __forceinline__ void fast_add(Fast& r, const u32x4 (&x)[U], float k) {
+    constexpr int N = Vec<T>::kN;
+    float m = r.m, low = kInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float a = Vec<T>::get(x[u], i), b = Vec<T>::get(x[u], i + 1);
+            m = fmaxf(fmaxf(m, a), b);
+            if (ENTROPY) low = fminf(fminf(low, a), b);
+        }
+    fast_rebase<ENTROPY>(r, m, k);
+    const bool masked = ENTROPY && __any(low == -kInf);  // d = -infinity, which t has to leave out
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float s[N], t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float d = __builtin_fmaf(Vec<T>::get(x[u], i), k, -r.c);
+            s[i] = exp2_raw(d);
+            if (ENTROPY) {
+                if (masked) d = fmaxf(d, kLowest);
+                t = __builtin_fmaf(s[i], d, t);
+            }
+        }
+#pragma unroll
+        for (int h = N / 2; h; h >>= 1)
+#pragma unroll
+            for (int i = 0; i < h; ++i) s[i] += s[i + h];
+        r.s += s[0];
+        r.t += t;
+    }
+}
+
+template <typename T, int THREADS, bool ENTROPY>
+__device__ __forceinline__ Fast fast_running(const T* row, int64_t vocab, float k) {
+    constexpr int N = Vec<T>::kN;
+    constexpr int U = 4;
+    const int64_t nv = vocab / N;
+    const uint32_t none = Vec<T>::kNegInf;
+    Fast r{-kInf, 0.0f, 0.0f, 0.0f};
+    int64_t v = threadIdx.x;
+    u32x4 x[U];
+    if (v + (U - 1) * THREADS < nv) {  // whole groups, the next one's loads ahead of each group's arithmetic
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = load_vec(row + (v + u * THREADS) * N);
+        while (true) {
+            const int64_t w = v + U * THREADS;
+            const bool more = w + (U - 1) * THREADS < nv;
+            u32x4 y[U];
+            if (more) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) y[u] = load_vec(row + (w + u * THREADS) * N);
+            }
+            fast_add<T, ENTROPY>(r, x, k);
+            v = w;
+            if (!more) break;
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = y[u];
+        }
+    }
+    if (v < nv) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            x[u] = v + u * THREADS < nv ? load_vec(row + (v + u * THREADS) * N) : u32x4{none, none, none, none};
+        fast_add<T, ENTROPY>(r, x, k);
+    }
+    const int64_t tail = nv * N + threadIdx.x;
+    if (tail < vocab) {
+        const float f = Vec<T>::one(row[tail]);
+        Fast o{f, base_of(f) * k, f == -kInf ? 0.0f : 1.0f, 0.0f};
+        const float d = __builtin_fmaf(f, k, -o.c);  // the rounding of c
+        if (f != -kInf) o.s = exp2_raw(d), o.t = o.s * d;
+        r = fast_merge<ENTROPY>(r, o, k);
+    }
+    return r;
+}
+
+template <int THREADS, bool ENTROPY>
+__device__ __forceinline__ Fast fast_block_merge(Fast r, float k, Fast* part) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const Fast o{__shfl_xor(r.m, d, 64), __shfl_xor(r.c, d, 64), __shfl_xor(r.s, d, 64),
+                     ENTROPY ? __shfl_xor(r.t, d, 64) : 0.0f};
+        r = fast_merge<ENTROPY>(r, o, k);
+    }
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = r;
+    __syncthreads();
+    r = part[threadIdx.x & (THREADS / 64 - 1)];
+#pragma unroll
+    for (int d = THREADS / 128; d; d >>= 1) {
+        const Fast o{__shfl_xor(r.m, d, 64), __shfl_xor(r.c, d, 64), __shfl_xor(r.s, d, 64),
+                     ENTROPY ? __shfl_xor(r.t, d, 64) : 0.0f};
+        r = fast_merge<ENTROPY>(r, o, k);
+    }
+    return r;
+}
+
+__device__ __forceinline__ bool ordinary(const Fast& r) {
+    return r.s > 0.0f && r.s < kInf && fabsf(r.c) < 1048576.0f && r.t == r.t;
+}
+
+// Statistics of a row, the same in every thread of the block: its maximum, log
+// s and t / s (d in powers of two), s relative to the maximum; own: this
+// thread's largest logit.
+struct RowStats {
+    float m, logsum, mean_d, own;
+};
+
+template <typename T, int THREADS, bool ENTROPY>
+__device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float k, Running* part) {
+    static_assert(sizeof(Fast) * (THREADS / 64) <= 1024, "part");
+    Fast* fpart = reinterpret_cast<Fast*>(part);
+    const Fast own = fast_running<T, THREADS, ENTROPY>(row, vocab, k);
+    const Fast r = fast_block_merge<THREADS, ENTROPY>(own, k, fpart);
+    if (ordinary(r)) {
+        // from c to the maximum: x k - c = (x - m) k + (m k - c)
+        const float shift = __builtin_fmaf(r.m, k, -r.c);
+        return RowStats{r.m, logf(r.s) - kLn2 * shift, ENTROPY ? r.t / r.s - shift : 0.0f, own.m};
+    }
+    __syncthreads();  // every thread has read the block's parts
+    const Running a = row_running<T, THREADS>(row, vocab, k);
+    const Running b = block_merge<THREADS>(a, k, part);
+    if (b.m == -kInf && b.s == 0.0f) return RowStats{-kInf, 0.0f, 0.0f, -kInf};
+    if (!(b.s < kInf)) return RowStats{b.m, quiet_nan(), quiet_nan(), a.m};
+    return RowStats{b.m, logf(b.s), b.t / b.s, a.m};
 }
 
 // ------------------------------------------------------------------ best alternatives
@@ -180,7 +327,7 @@ __device__ __forceinline__ bool before(float a, int i, float b, int j) { return 
 // The thread's first element that comes after (x0, i0) in the order of
 // `before`; token INT32_MAX if there is none.
 template <typename T, int THREADS>
-__device__ __forceinline__ void next_own(const T* __restrict__ row, int64_t vocab, float x0, int i0, float* best,
+__device__ __forceinline__ void next_own(const T* row, int64_t vocab, float x0, int i0, float* best,
                                          int* best_i) {
     constexpr int N = Vec<T>::kN;
     const int64_t nv = vocab / N;
@@ -215,7 +362,7 @@ __device__ __forceinline__ void next_own(const T* __restrict__ row, int64_t voca
 // thread it came from looks for its next. Right for any row (equal or masked
 // logits included). Every logit is below +infinity and no NaN.
 template <typename T, int THREADS>
-__device__ __forceinline__ void top_by_rounds(const T* __restrict__ row, int64_t vocab, int top, float m, float inv_t,
+__device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int top, float m, float inv_t,
                                               float logsum, int32_t* ids, float* lps, float* lx, int* li) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float b;
@@ -252,17 +399,95 @@ __device__ __forceinline__ void top_by_rounds(const T* __restrict__ row, int64_t
     }
 }
 
-// ------------------------------------------------------------------ log-probabilities
-
-constexpr int kRowThreads = 256;
+// The row's `top` best elements. 64 groups of threads cover the row; the
+// top-th largest of the groups' maxima is a bound that at least `top` elements
+// reach and, the elements being spread over the groups, few more do: the
+// threads whose own maximum reaches it read their elements again (they come
+// from a cache) and list those that do, and the list is ranked by counting. A
+// row with more of them than the list holds (equal logits, most of the
+// vocabulary masked, an order by size) goes by rounds.
+constexpr int kListed = 512;
+struct TopShared {
+    float group[64];
+    float x[kListed];
+    int id[kListed];
+    int n;
+};
 
 template <typename T, int THREADS>
+__device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int top, const RowStats& st, float inv_t,
+                                             int32_t* ids, float* lps, TopShared& sh) {
+    constexpr int N = Vec<T>::kN;
+    constexpr int kGroup = THREADS / 64;  // threads a group
+    const int lane = threadIdx.x & 63;
+    float g = st.own;
+#pragma unroll
+    for (int d = 1; d < kGroup; d <<= 1) g = fmaxf(g, __shfl_xor(g, d, 64));
+    if (threadIdx.x % kGroup == 0) sh.group[threadIdx.x / kGroup] = g;
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    g = sh.group[lane];
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
+        rank += before(o, i, g, lane);
+    }
+    const float bound = __shfl(g, __ffsll(__ballot(rank == top - 1)) - 1, 64);
+    auto list = [&](float f, int64_t at) {
+        if (f >= bound) {
+            const int n = atomicAdd(&sh.n, 1);
+            if (n < kListed) {
+                sh.x[n] = f;
+                sh.id[n] = (int)at;
+            }
+        }
+    };
+    if (st.own >= bound) {
+        const int64_t nv = vocab / N;
+        constexpr int U = 8;
+        for (int64_t v = threadIdx.x; v < nv; v += U * THREADS) {
+            u32x4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t none = Vec<T>::kNan;
+                x[u] = v + u * THREADS < nv ? load_vec(row + (v + u * THREADS) * N) : u32x4{none, none, none, none};
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < N; ++i) list(Vec<T>::get(x[u], i), (v + u * THREADS) * N + i);
+        }
+        const int64_t tail = nv * N + threadIdx.x;
+        if (tail < vocab) list(Vec<T>::one(row[tail]), tail);
+    }
+    __syncthreads();
+    const int n = sh.n;
+    if (n > kListed) {
+        __syncthreads();
+        top_by_rounds<T, THREADS>(row, vocab, top, st.m, inv_t, st.logsum, ids, lps, sh.x, sh.id);
+        return;
+    }
+    for (int c = threadIdx.x; c < n; c += THREADS) {
+        const float x = sh.x[c];
+        const int id = sh.id[c];
+        int place = 0;
+        for (int o = 0; o < n; ++o) place += before(sh.x[o], sh.id[o], x, id);
+        if (place < top) {
+            ids[place] = id;
+            lps[place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ log-probabilities
+
+template <typename T, int THREADS, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logits, int64_t stride, int64_t vocab,
                                                       const int32_t* __restrict__ tokens, float inv_t, float k,
                                                       LogprobsOut out) {
-    __shared__ Running part[THREADS / 64];
-    __shared__ float lx[THREADS / 64];
-    __shared__ int li[THREADS / 64];
+    __shared__ Running part[1024 / sizeof(Running)];
+    __shared__ TopShared sh;
     const int64_t r = blockIdx.x;
     const T* row = logits + r * stride;
     const int64_t token = tokens[r];
@@ -280,20 +505,19 @@ __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logi
         }
         return;
     }
-    const Running a = block_merge<THREADS>(row_running<T, THREADS, 4>(row, vocab, k), k, part);
-    const bool empty = a.m == -kInf && a.s == 0.0f;
-    const bool bad = !(a.s < kInf);  // a NaN or +infinity in the row
-    const float logsum = empty ? 0.0f : bad ? quiet_nan() : logf(a.s);
+    const RowStats st = row_stats<T, THREADS, ENTROPY>(row, vocab, k, part);
+    const bool empty = st.m == -kInf;
+    const bool bad = !(st.logsum < kInf);  // a NaN or +infinity in the row
     if (threadIdx.x == 0) {
         if (out.logprob) {
             float lp = quiet_nan();
-            if (token < vocab) lp = empty ? -kInf : (Vec<T>::one(row[token]) - a.m) * inv_t - logsum;
+            if (token < vocab) lp = empty ? -kInf : (Vec<T>::one(row[token]) - st.m) * inv_t - st.logsum;
             out.logprob[r] = lp;
         }
-        if (out.entropy) out.entropy[r] = empty ? 0.0f : logsum - kLn2 * (a.t / a.s);
+        if (out.entropy) out.entropy[r] = st.logsum - kLn2 * st.mean_d;
         if (out.stats) {
-            out.stats[2 * r] = a.m;
-            out.stats[2 * r + 1] = logsum;
+            out.stats[2 * r] = st.m;
+            out.stats[2 * r + 1] = st.logsum;
         }
     }
     if (out.top == 0) return;
@@ -304,7 +528,7 @@ __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logi
         }
         return;
     }
-    top_by_rounds<T, THREADS>(row, vocab, out.top, a.m, inv_t, logsum, ids, lps, lx, li);
+    top_elements<T, THREADS>(row, vocab, out.top, st, inv_t, ids, lps, sh);
 }
 
 // ------------------------------------------------------------------ gradient of the log-probabilities
@@ -355,6 +579,8 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
 }
 
 // ------------------------------------------------------------------ distillation
+
+constexpr int kRowThreads = 256;
 
 template <int THREADS>
 __device__ __forceinline__ float block_sum(float v, float* part) {
@@ -433,7 +659,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     }
     qs = block_sum<THREADS>(qs, fpart);
     const float inv_qs = 1.0f / qs, logqs = logf(qs);
-    const Running a = block_merge<THREADS>(row_running<T, THREADS, 4>(row, vocab, k), k, part);
+    const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, part);
     const float m = base_of(a.m);
     const float logsum = logf(a.s), inv_s = a.s == 0.0f ? 0.0f : 1.0f / a.s;
     // loss: log q - log p = (t - tmax) / T - (x - m) / T + (log s - log sum of q's)
@@ -479,16 +705,35 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
 
 }  // namespace
 
+namespace {
+
+template <typename T, int THREADS>
+void run_logprobs(Rows logits, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
+                  const LogprobsOut& out, hipStream_t s) {
+    const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
+    const T* p = static_cast<const T*>(logits.p);
+    if (out.entropy)
+        hipLaunchKernelGGL((k_logprobs<T, THREADS, true>), dim3((unsigned)rows), dim3(THREADS), 0, s, p, logits.stride,
+                           vocab, tokens, inv_t, k, out);
+    else
+        hipLaunchKernelGGL((k_logprobs<T, THREADS, false>), dim3((unsigned)rows), dim3(THREADS), 0, s, p,
+                           logits.stride, vocab, tokens, inv_t, k, out);
+}
+
+}  // namespace
+
 int launch_logprobs(Rows logits, int dtype, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
                     const LogprobsOut& out, void* stream) {
-    const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
     hipStream_t s = (hipStream_t)stream;
-    if (dtype == ZS_DTYPE_BF16)
-        hipLaunchKernelGGL((k_logprobs<uint16_t, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
-                           static_cast<const uint16_t*>(logits.p), logits.stride, vocab, tokens, inv_t, k, out);
+    const bool few = rows <= 512 && vocab > 4096;
+    if (dtype == ZS_DTYPE_BF16 && few)
+        run_logprobs<uint16_t, 1024>(logits, rows, vocab, tokens, temperature, out, s);
+    else if (dtype == ZS_DTYPE_BF16)
+        run_logprobs<uint16_t, 256>(logits, rows, vocab, tokens, temperature, out, s);
+    else if (few)
+        run_logprobs<float, 1024>(logits, rows, vocab, tokens, temperature, out, s);
     else
-        hipLaunchKernelGGL((k_logprobs<float, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
-                           static_cast<const float*>(logits.p), logits.stride, vocab, tokens, inv_t, k, out);
+        run_logprobs<float, 256>(logits, rows, vocab, tokens, temperature, out, s);
     return (int)hipGetLastError();
 }
 
