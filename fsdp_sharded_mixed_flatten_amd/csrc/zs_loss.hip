@@ -30,12 +30,12 @@ constexpr float kLowest = -1.0e4f;
 
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
 
-// fp32 -> bf16 bits, round to nearest even (the one rounding of a stored
-// gradient); NaN stays NaN.
-__device__ __forceinline__ uint32_t f32_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    return ((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r;
+// Two fp32 values as bf16 in one word, round to nearest even by the hardware's
+// conversion (the one rounding of a stored gradient); NaN stays NaN.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
 // A 16-byte vector of logits as fp32 values and back.
@@ -48,11 +48,11 @@ struct Vec<uint16_t> {
         return __uint_as_float((i & 1) ? (v[i >> 1] & 0xFFFF0000u) : (v[i >> 1] << 16));
     }
     static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-    static __device__ __forceinline__ uint16_t round(float f) { return (uint16_t)f32_bf16(f); }
+    static __device__ __forceinline__ uint16_t round(float f) { return (uint16_t)pack_bf16(f, f); }
     static __device__ __forceinline__ u32x4 pack(const float* f) {
         u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = f32_bf16(f[2 * i]) | (f32_bf16(f[2 * i + 1]) << 16);
+        for (int i = 0; i < 4; ++i) v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
         return v;
     }
     static constexpr uint32_t kNegInf = 0xFF80FF80u, kNan = 0x7FC07FC0u;
@@ -190,6 +190,14 @@ __device__ __forceinline__ Fast fast_merge(Fast a, Fast b, float k) {
     return Fast{a.m, a.c, a.s + b.s, a.t + b.t};
 }
 
+__device__ __forceinline__ Fast fast_one(float x, float k) {
+    if (x == -kInf) return Fast{x, 0.0f, 0.0f, 0.0f};
+    const float c = x * k;
+    const float d = __builtin_fmaf(x, k, -c);  // the rounding of c
+    const float e = exp2_raw(d);
+    return Fast{x, c, e, e * d};
+}
+
 template <typename T, bool ENTROPY, int U>
 __device__ __forceinline__ void fast_add(Fast& r, const u32x4 (&x)[U], float k) {
     constexpr int N = Vec<T>::kN;
@@ -260,11 +268,7 @@ __device__ __forceinline__ Fast fast_running(const T* row, int64_t vocab, float 
     }
     const int64_t tail = nv * N + threadIdx.x;
     if (tail < vocab) {
-        const float f = Vec<T>::one(row[tail]);
-        Fast o{f, base_of(f) * k, f == -kInf ? 0.0f : 1.0f, 0.0f};
-        const float d = __builtin_fmaf(f, k, -o.c);  // the rounding of c
-        if (f != -kInf) o.s = exp2_raw(d), o.t = o.s * d;
-        r = fast_merge<ENTROPY>(r, o, k);
+        r = fast_merge<ENTROPY>(r, fast_one(Vec<T>::one(row[tail]), k), k);
     }
     return r;
 }
@@ -580,8 +584,6 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
 
 // ------------------------------------------------------------------ distillation
 
-constexpr int kRowThreads = 256;
-
 template <int THREADS>
 __device__ __forceinline__ float block_sum(float v, float* part) {
 #pragma unroll
@@ -608,99 +610,199 @@ __device__ __forceinline__ float block_max(float v, float* part) {
 
 template <typename T>
 __device__ __forceinline__ void fill_row(T* g, int64_t vocab, float f) {
-    for (int64_t j = threadIdx.x; j < vocab; j += blockDim.x) g[j] = Vec<T>::round(f);
+    constexpr int N = Vec<T>::kN;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = f;
+    const u32x4 x = Vec<T>::pack(v);
+    const int64_t nv = vocab / N;
+    for (int64_t j = threadIdx.x; j < nv; j += blockDim.x) store_vec(g + j * N, x);
+    const int64_t tail = nv * N + threadIdx.x;
+    if (tail < vocab) g[tail] = Vec<T>::round(f);
 }
 
-// One block per row: the teacher's distribution into shared memory, the
-// student's running softmax, the loss, then the gradient in a second pass over
-// the row and the teacher's entries set right in it.
+struct DistillShared {
+    float q[ZS_DISTILL_MAX_K];  // the teacher's distribution
+    float x[ZS_DISTILL_MAX_K];  // the student's logits at its tokens
+    int32_t id[ZS_DISTILL_MAX_K];
+    float fpart[16];
+    Running part[16];
+};
+
+enum TeacherRow { kTeacherUsed, kTeacherEmpty, kTeacherBad };
+
+// The teacher's entries of a row into shared memory (sh.q holds its logits, of
+// unused entries -infinity), its largest logit and the log of the sum of its
+// exponentials.
 template <typename T, int THREADS>
+__device__ __forceinline__ TeacherRow teacher_row(const T* row, int64_t vocab, const Teacher& te, int64_t r, float k,
+                                                  DistillShared& sh, float* tmax_out, float* logq_out) {
+    const int32_t* ids = te.ids + r * te.k;
+    const float* tl = te.logits + r * te.k;
+    float tmax = -kInf, bad = 0.0f;
+    for (int i = threadIdx.x; i < te.k; i += THREADS) {
+        const int32_t j = ids[i];
+        const float t = j < 0 ? -kInf : tl[i];
+        sh.id[i] = j;
+        sh.q[i] = t;
+        sh.x[i] = j >= 0 && j < vocab ? Vec<T>::one(row[j]) : 0.0f;
+        tmax = fmaxf(tmax, t);
+        if (j >= vocab || !(t < kInf)) bad = 1.0f;
+    }
+    tmax = block_max<THREADS>(tmax, sh.fpart);
+    bad = block_max<THREADS>(bad, sh.fpart);
+    if (bad != 0.0f) return kTeacherBad;
+    if (tmax == -kInf) return kTeacherEmpty;
+    float sum = 0.0f;
+    for (int i = threadIdx.x; i < te.k; i += THREADS) sum += exp2f((sh.q[i] - tmax) * k);
+    sum = block_sum<THREADS>(sum, sh.fpart);
+    *tmax_out = tmax;
+    *logq_out = logf(sum);
+    return kTeacherUsed;
+}
+
+// loss / T^2 = sum of q ((t - tmax) / T - (x - m) / T + log s - log sum of the
+// teacher's exponentials); sh.q turns from the teacher's logits into q.
+template <int THREADS>
+__device__ __forceinline__ float teacher_loss(int n, float tmax, float logq, float m, float logsum, float inv_t,
+                                              float k, DistillShared& sh) {
+    float l = 0.0f;
+    const float inv = exp2f(-logq * (1.0f / kLn2));
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const float dt = sh.q[i] - tmax;
+        const float q = exp2f(dt * k) * inv;
+        sh.q[i] = q;
+        if (q > 0.0f) l += q * ((dt - (sh.x[i] - m)) * inv_t + (logsum - logq));
+    }
+    return block_sum<THREADS>(l, sh.fpart);
+}
+
+// The entries' tokens are written again with the teacher's share, once for each
+// token by the first of its entries. p(x): the student's share of the
+// gradient. Behind a barrier after the row's gradient.
+template <typename T, int THREADS, typename P>
+__device__ __forceinline__ void teacher_gradient(int n, float scale, T* g, const DistillShared& sh, P p) {
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        if (!(sh.q[i] > 0.0f)) continue;
+        const int id = sh.id[i];
+        float q = 0.0f;
+        bool first = true;
+        for (int j = 0; j < n; ++j) {
+            const bool same = sh.id[j] == id && sh.q[j] > 0.0f;
+            if (same) q += sh.q[j];
+            first = first && !(same && j < i);
+        }
+        if (first) g[id] = Vec<T>::round(p(sh.x[i]) - scale * q);
+    }
+}
+
+// One block per row. NV > 0: the row's vectors are held in registers (up to NV
+// a thread) between the pass that sums their exponentials as they arrive and
+// the pass that writes the gradient, so logits are read once; 0: the second
+// pass reads them again.
+template <typename T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t stride, int64_t vocab, Teacher te,
                                                      float temperature, float inv_t, float k,
                                                      float* __restrict__ loss, T* grad, int64_t grad_stride) {
     constexpr int N = Vec<T>::kN;
-    __shared__ Running part[THREADS / 64];
-    __shared__ float fpart[THREADS / 64];
-    __shared__ float q[ZS_DISTILL_MAX_K];
-    __shared__ float xs[ZS_DISTILL_MAX_K];
-    __shared__ int32_t id[ZS_DISTILL_MAX_K];
+    __shared__ DistillShared sh;
     const int64_t r = blockIdx.x;
     const T* row = logits + r * stride;
     T* g = grad + r * grad_stride;
-    const int32_t* ids = te.ids + r * te.k;
-    const float* tl = te.logits + r * te.k;
     const float w = te.row_weight ? te.row_weight[r] : 1.0f;
-    // the teacher's largest logit; 0 x of it is NaN where one is NaN or +infinity
-    float tmax = -kInf, bad = 0.0f;
-    for (int i = threadIdx.x; i < te.k; i += THREADS) {
-        const int32_t j = ids[i];
-        id[i] = j;
-        if (j < 0) continue;
-        tmax = fmaxf(tmax, tl[i]);
-        if (j >= vocab || !(tl[i] < kInf)) bad = 1.0f;
-    }
-    tmax = block_max<THREADS>(tmax, fpart);
-    bad = block_max<THREADS>(bad, fpart);
-    if (w == 0.0f || (tmax == -kInf && bad == 0.0f)) {
+    if (w == 0.0f) {
         if (threadIdx.x == 0) loss[r] = 0.0f;
         if (grad) fill_row(g, vocab, 0.0f);
         return;
     }
-    if (bad != 0.0f) {
-        if (threadIdx.x == 0) loss[r] = quiet_nan();
-        if (grad) fill_row(g, vocab, quiet_nan());
+    const int64_t nv = vocab / N;
+    const int64_t tail = nv * N + threadIdx.x;
+    constexpr int kHeld = NV > 0 ? NV : 1;
+    u32x4 x[kHeld];
+    if (NV > 0) {
+        const uint32_t none = Vec<T>::kNegInf;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t v = threadIdx.x + i * THREADS;
+            x[i] = v < nv ? load_vec(row + v * N) : u32x4{none, none, none, none};
+        }
+    }
+    float tmax, logq;
+    const TeacherRow kind = teacher_row<T, THREADS>(row, vocab, te, r, k, sh, &tmax, &logq);
+    if (kind != kTeacherUsed) {
+        const float f = kind == kTeacherBad ? quiet_nan() : 0.0f;
+        if (threadIdx.x == 0) loss[r] = f;
+        if (grad) fill_row(g, vocab, f);
         return;
     }
-    float qs = 0.0f;
-    for (int i = threadIdx.x; i < te.k; i += THREADS) {
-        const float e = id[i] < 0 ? 0.0f : exp2f((tl[i] - tmax) * k);
-        q[i] = e;
-        qs += e;
-    }
-    qs = block_sum<THREADS>(qs, fpart);
-    const float inv_qs = 1.0f / qs, logqs = logf(qs);
-    const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, part);
-    const float m = base_of(a.m);
-    const float logsum = logf(a.s), inv_s = a.s == 0.0f ? 0.0f : 1.0f / a.s;
-    // loss: log q - log p = (t - tmax) / T - (x - m) / T + (log s - log sum of q's)
-    float l = 0.0f;
-    for (int i = threadIdx.x; i < te.k; i += THREADS) {
-        const float qi = q[i] * inv_qs;
-        q[i] = qi;
-        if (!(qi > 0.0f)) continue;
-        const float x = Vec<T>::one(row[id[i]]);
-        xs[i] = x;
-        l += qi * (((tl[i] - tmax) - (x - m)) * inv_t + (logsum - logqs));
-    }
-    l = block_sum<THREADS>(l, fpart);
-    if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf ? kInf : l);
-    if (!grad) return;
-    const float scale = w * temperature;
-    const float c = scale * inv_s;
-    const int64_t nv = vocab / N;
-    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
-        const u32x4 x = load_vec(row + v * N);
-        float f[N];
+    Fast f{-kInf, 0.0f, 0.0f, 0.0f};
+    if (NV > 0) {
+        constexpr int U = NV % 4 == 0 ? 4 : 1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = c * exp2f((Vec<T>::get(x, i) - m) * k);
-        store_vec(g + v * N, Vec<T>::pack(f));
+        for (int i = 0; i < NV; i += U) {
+            u32x4 y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) y[u] = x[i + u];
+            fast_add<T, false>(f, y, k);
+            __builtin_amdgcn_sched_barrier(0);  // the held vectors leave no registers for a second group in flight
+        }
+        if (tail < vocab) f = fast_merge<false>(f, fast_one(Vec<T>::one(row[tail]), k), k);
+    } else {
+        f = fast_running<T, THREADS, false>(row, vocab, k);
     }
-    const int64_t tail = nv * N + threadIdx.x;
-    if (tail < vocab) g[tail] = Vec<T>::round(c * exp2f((Vec<T>::one(row[tail]) - m) * k));
-    // the entries' tokens: written again with the teacher's share, once for
-    // each token by the first of its entries
+    f = fast_block_merge<THREADS, false>(f, k, reinterpret_cast<Fast*>(sh.part));
+    const float scale = w * temperature;
+    if (ordinary(f)) {
+        const float l = teacher_loss<THREADS>(te.k, tmax, logq, f.m,
+                                              logf(f.s) - kLn2 * __builtin_fmaf(f.m, k, -f.c), inv_t, k, sh);
+        if (threadIdx.x == 0) loss[r] = w * temperature * temperature * l;
+        if (!grad) return;
+        const float c = scale / f.s;
+        auto p = [&](float z) { return c * exp2_raw(__builtin_fmaf(z, k, -f.c)); };
+        if (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t v = threadIdx.x + i * THREADS;
+                float o[N];
+                asm("" : "+v"(x[i]));  // unpacked again here: the first pass's fp32 values are not kept
+#pragma unroll
+                for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[i], j));
+                if (v < nv) store_vec(g + v * N, Vec<T>::pack(o));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
+                const u32x4 y = load_vec(row + v * N);
+                float o[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(y, j));
+                store_vec(g + v * N, Vec<T>::pack(o));
+            }
+        }
+        if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
+        __syncthreads();
+        teacher_gradient<T, THREADS>(te.k, scale, g, sh, p);
+        return;
+    }
+    // any other row: differences from the maximum first, the row read again
     __syncthreads();
-    for (int i = threadIdx.x; i < te.k; i += THREADS) {
-        if (!(q[i] > 0.0f)) continue;
-        bool first = true;
-        for (int j = 0; j < i; ++j)
-            if (id[j] == id[i] && q[j] > 0.0f) first = false;
-        if (!first) continue;
-        float qi = q[i];
-        for (int j = i + 1; j < te.k; ++j)
-            if (id[j] == id[i]) qi += q[j];
-        g[id[i]] = Vec<T>::round(c * exp2f((xs[i] - m) * k) - scale * qi);
+    const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, sh.part);
+    const float m = base_of(a.m);
+    const float l = teacher_loss<THREADS>(te.k, tmax, logq, m, logf(a.s), inv_t, k, sh);
+    if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf && a.s == 0.0f ? kInf : l);
+    if (!grad) return;
+    const float c = a.s == 0.0f ? 0.0f : scale / a.s;
+    auto p = [&](float z) { return c * exp2f((z - m) * k); };
+    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
+        const u32x4 y = load_vec(row + v * N);
+        float o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(y, j));
+        store_vec(g + v * N, Vec<T>::pack(o));
     }
+    if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
+    __syncthreads();
+    teacher_gradient<T, THREADS>(te.k, scale, g, sh, p);
 }
 
 }  // namespace
@@ -763,19 +865,44 @@ int launch_logprobs_grad(Rows logits, int dtype, int64_t rows, int64_t vocab, do
     return run_grad<float>(logits, rows, vocab, temperature, in, grad, grad_stride, (hipStream_t)stream);
 }
 
+namespace {
+
+template <typename T, int THREADS, int NV>
+void run_distill(Rows logits, int64_t rows, int64_t vocab, const Teacher& t, double temperature, float* loss,
+                 void* grad, int64_t grad_stride, hipStream_t s) {
+    hipLaunchKernelGGL((k_distill<T, THREADS, NV>), dim3((unsigned)rows), dim3(THREADS), 0, s,
+                       static_cast<const T*>(logits.p), logits.stride, vocab, t, (float)temperature,
+                       (float)(1.0 / temperature), (float)(M_LOG2E / temperature), loss, static_cast<T*>(grad),
+                       grad_stride);
+}
+
+template <typename T>
+int pick_distill(Rows logits, int64_t rows, int64_t vocab, const Teacher& t, double temperature, float* loss,
+                 void* grad, int64_t grad_stride, hipStream_t s) {
+    const int64_t nv = vocab / Vec<T>::kN;  // 16-byte vectors of a row
+    if (nv <= 256 * 4)
+        run_distill<T, 256, 4>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else if (nv <= 256 * 16)
+        run_distill<T, 256, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else if (nv <= 512 * 16)
+        run_distill<T, 512, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else if (nv <= 1024 * 16)
+        run_distill<T, 1024, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else if (nv <= 1024 * 20)
+        run_distill<T, 1024, 20>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else
+        run_distill<T, 1024, 0>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+
 int launch_distill(Rows logits, int dtype, int64_t rows, int64_t vocab, const Teacher& t, double temperature,
                    float* loss, void* grad, int64_t grad_stride, void* stream) {
-    const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
-    hipStream_t s = (hipStream_t)stream;
     if (dtype == ZS_DTYPE_BF16)
-        hipLaunchKernelGGL((k_distill<uint16_t, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
-                           static_cast<const uint16_t*>(logits.p), logits.stride, vocab, t, (float)temperature, inv_t,
-                           k, loss, static_cast<uint16_t*>(grad), grad_stride);
-    else
-        hipLaunchKernelGGL((k_distill<float, kRowThreads>), dim3((unsigned)rows), dim3(kRowThreads), 0, s,
-                           static_cast<const float*>(logits.p), logits.stride, vocab, t, (float)temperature, inv_t, k,
-                           loss, static_cast<float*>(grad), grad_stride);
-    return (int)hipGetLastError();
+        return pick_distill<uint16_t>(logits, rows, vocab, t, temperature, loss, grad, grad_stride,
+                                      (hipStream_t)stream);
+    return pick_distill<float>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, (hipStream_t)stream);
 }
 
 }  // namespace zs
