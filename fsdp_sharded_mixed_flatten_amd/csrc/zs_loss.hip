@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "zs_lm_internal.h"
 
@@ -77,6 +78,28 @@ template <typename T>
 __device__ __forceinline__ void store_vec(T* p, u32x4 v) {
     *reinterpret_cast<u32x4_u2*>(p) = v;
 }
+
+// Vector `first` + threadIdx.x of a row: the same row and `first` in the whole
+// block, so that the address is a scalar and one 32-bit offset a thread.
+template <typename T>
+__device__ __forceinline__ u32x4 load_at(const T* row, int64_t first) {
+    return *reinterpret_cast<const u32x4_u2*>(reinterpret_cast<const char*>(row) + first * 16 + threadIdx.x * 16u);
+}
+// NT: nontemporal.
+template <bool NT, typename T>
+__device__ __forceinline__ void store_at(T* row, int64_t first, u32x4 v) {
+    u32x4_u2* p = reinterpret_cast<u32x4_u2*>(reinterpret_cast<char*>(row) + first * 16 + threadIdx.x * 16u);
+    if (NT)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
+// Gradients are not read here again: nontemporal stores leave the caches to the
+// logits (4096 x 32000 bf16 87 us against 107, 1024 x 151936 fp32 321 against
+// 381). Not where rows start inside a 16-byte unit: a line then takes two
+// stores, and they no longer meet in a cache (301 x 100003 fp32 62 against 59).
+__device__ __forceinline__ bool whole_units(const void* g) { return (reinterpret_cast<uintptr_t>(g) & 15) == 0; }
 
 // ------------------------------------------------------------------ running softmax
 // max m of the logits, s = sum of 2^((x - m) k) and t = sum of 2^d d with
@@ -237,21 +260,21 @@ template <typename T, int THREADS, bool ENTROPY>
 __device__ __forceinline__ Fast fast_running(const T* row, int64_t vocab, float k) {
     constexpr int N = Vec<T>::kN;
     constexpr int U = 4;
-    const int64_t nv = vocab / N;
+    const int nv = (int)(vocab / N), tid = threadIdx.x;
     const uint32_t none = Vec<T>::kNegInf;
     Fast r{-kInf, 0.0f, 0.0f, 0.0f};
-    int64_t v = threadIdx.x;
+    int v = 0;  // of the block's first thread
     u32x4 x[U];
-    if (v + (U - 1) * THREADS < nv) {  // whole groups, the next one's loads ahead of each group's arithmetic
+    if (v + U * THREADS <= nv) {  // whole groups, the next one's loads ahead of each group's arithmetic
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = load_vec(row + (v + u * THREADS) * N);
+        for (int u = 0; u < U; ++u) x[u] = load_at(row, v + u * THREADS);
         while (true) {
-            const int64_t w = v + U * THREADS;
-            const bool more = w + (U - 1) * THREADS < nv;
+            const int w = v + U * THREADS;
+            const bool more = w + U * THREADS <= nv;
             u32x4 y[U];
             if (more) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) y[u] = load_vec(row + (w + u * THREADS) * N);
+                for (int u = 0; u < U; ++u) y[u] = load_at(row, w + u * THREADS);
             }
             fast_add<T, ENTROPY>(r, x, k);
             v = w;
@@ -262,14 +285,14 @@ __device__ __forceinline__ Fast fast_running(const T* row, int64_t vocab, float 
     }
     if (v < nv) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            x[u] = v + u * THREADS < nv ? load_vec(row + (v + u * THREADS) * N) : u32x4{none, none, none, none};
+        for (int u = 0; u < U; ++u) {
+            x[u] = u32x4{none, none, none, none};
+            if (v + u * THREADS + tid < nv) x[u] = load_at(row, v + u * THREADS);
+        }
         fast_add<T, ENTROPY>(r, x, k);
     }
-    const int64_t tail = nv * N + threadIdx.x;
-    if (tail < vocab) {
-        r = fast_merge<ENTROPY>(r, fast_one(Vec<T>::one(row[tail]), k), k);
-    }
+    const int tail = nv * N + tid;
+    if (tail < vocab) r = fast_merge<ENTROPY>(r, fast_one(Vec<T>::one(row[tail]), k), k);
     return r;
 }
 
@@ -406,8 +429,10 @@ __device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int t
 // The row's `top` best elements. 64 groups of threads cover the row; the
 // top-th largest of the groups' maxima is a bound that at least `top` elements
 // reach and, the elements being spread over the groups, few more do: the
-// threads whose own maximum reaches it read their elements again (they come
-// from a cache) and list those that do, and the list is ranked by counting. A
+// elements of the threads whose own maximum reaches it are read again (they
+// come from a cache), those that reach it are listed, and the list is ranked by
+// counting. The second reading is dealt out over the whole block: left to the
+// threads themselves it was a chain of loads a few lanes wide. A
 // row with more of them than the list holds (equal logits, most of the
 // vocabulary masked, an order by size) goes by rounds.
 constexpr int kListed = 512;
@@ -415,7 +440,8 @@ struct TopShared {
     float group[64];
     float x[kListed];
     int id[kListed];
-    int n;
+    int owner[512];
+    int n, owners;
 };
 
 template <typename T, int THREADS>
@@ -428,42 +454,57 @@ __device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int to
 #pragma unroll
     for (int d = 1; d < kGroup; d <<= 1) g = fmaxf(g, __shfl_xor(g, d, 64));
     if (threadIdx.x % kGroup == 0) sh.group[threadIdx.x / kGroup] = g;
-    if (threadIdx.x == 0) sh.n = 0;
+    if (threadIdx.x == 0) sh.n = sh.owners = 0;
     __syncthreads();
+    // the bound: the smallest group maximum that fewer than `top` others exceed
     g = sh.group[lane];
-    int rank = 0;
+    int above = 0;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i)) > g;
+    float bound = above < top ? g : kInf;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
-        rank += before(o, i, g, lane);
-    }
-    const float bound = __shfl(g, __ffsll(__ballot(rank == top - 1)) - 1, 64);
-    auto list = [&](float f, int64_t at) {
+    for (int d = 32; d; d >>= 1) bound = fminf(bound, __shfl_xor(bound, d, 64));
+    auto list = [&](float f, int at) {
         if (f >= bound) {
             const int n = atomicAdd(&sh.n, 1);
             if (n < kListed) {
                 sh.x[n] = f;
-                sh.id[n] = (int)at;
+                sh.id[n] = at;
             }
         }
     };
+    const int64_t nv = vocab / N;
     if (st.own >= bound) {
-        const int64_t nv = vocab / N;
-        constexpr int U = 8;
-        for (int64_t v = threadIdx.x; v < nv; v += U * THREADS) {
-            u32x4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t none = Vec<T>::kNan;
-                x[u] = v + u * THREADS < nv ? load_vec(row + (v + u * THREADS) * N) : u32x4{none, none, none, none};
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < N; ++i) list(Vec<T>::get(x[u], i), (v + u * THREADS) * N + i);
-        }
+        sh.owner[atomicAdd(&sh.owners, 1)] = threadIdx.x;
         const int64_t tail = nv * N + threadIdx.x;
-        if (tail < vocab) list(Vec<T>::one(row[tail]), tail);
+        if (tail < vocab) list(Vec<T>::one(row[tail]), (int)tail);
+    }
+    __syncthreads();
+    // the listed threads' vectors, dealt out over the block: vector j of thread
+    // o is o + j * THREADS
+    const unsigned per = (unsigned)((nv + THREADS - 1) / THREADS), all = per * sh.owners;
+    constexpr int U = 4;
+    for (unsigned p0 = threadIdx.x; p0 < all; p0 += U * THREADS) {
+        u32x4 x[U];
+        int64_t v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned p = p0 + u * THREADS;
+            const uint32_t none = Vec<T>::kNan;
+            v[u] = p < all ? sh.owner[p / per] + (int64_t)(p % per) * THREADS : nv;
+            x[u] = u32x4{none, none, none, none};
+            if (v[u] < nv) x[u] = load_vec(row + v[u] * N);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            unsigned reach = 0;  // few do: those are read once more rather than picked from registers
+#pragma unroll
+            for (int i = 0; i < N; ++i) reach |= Vec<T>::get(x[u], i) >= bound ? 1u << i : 0u;
+            for (; reach; reach &= reach - 1) {
+                const int at = (int)v[u] * N + __ffs(reach) - 1;
+                list(Vec<T>::one(row[at]), at);
+            }
+        }
     }
     __syncthreads();
     const int n = sh.n;
@@ -472,15 +513,30 @@ __device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int to
         top_by_rounds<T, THREADS>(row, vocab, top, st.m, inv_t, st.logsum, ids, lps, sh.x, sh.id);
         return;
     }
+    auto put = [&](int place, float x, int id) {
+        if (place < top) {
+            ids[place] = id;
+            lps[place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+        }
+    };
+    if (n <= 64) {  // the usual list: one wave, an entry a lane
+        if (threadIdx.x >= 64) return;
+        const float x = sh.x[lane];
+        const int id = sh.id[lane];
+        int place = 0;
+        for (int o = 0; o < n; ++o) {
+            const float ox = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), o));
+            place += before(ox, (int)__builtin_amdgcn_readlane(id, o), x, id);
+        }
+        if (lane < n) put(place, x, id);
+        return;
+    }
     for (int c = threadIdx.x; c < n; c += THREADS) {
         const float x = sh.x[c];
         const int id = sh.id[c];
         int place = 0;
         for (int o = 0; o < n; ++o) place += before(sh.x[o], sh.id[o], x, id);
-        if (place < top) {
-            ids[place] = id;
-            lps[place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
-        }
+        put(place, x, id);
     }
 }
 
@@ -555,7 +611,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
     const float gl = token >= vocab ? quiet_nan() : in.grad_logprob[r];
     const float gh = in.grad_entropy ? in.grad_entropy[r] : 0.0f;
     const float h = in.grad_entropy ? in.entropy[r] : 0.0f;
-    const int64_t nv = vocab / N;
+    const int nv = (int)(vocab / N), tid = threadIdx.x;
     // -(g_l + g_h (l + H)) p / T + [j == t] g_l / T
     auto value = [&](float x, int64_t j) {
         if (zero) return 0.0f;
@@ -565,46 +621,45 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
         const float hot = j == token ? gl : 0.0f;
         return (hot - p * (gl + gh * (fmaxf(l, kLowest) + h))) * inv_t;
     };
-    const int64_t v0 = tile * (kGradThreads * kGradU) + threadIdx.x;
+    const int v0 = (int)tile * (kGradThreads * kGradU);
+    u32x4 x[kGradU];
 #pragma unroll
     for (int u = 0; u < kGradU; ++u) {
-        const int64_t v = v0 + u * kGradThreads;
-        if (v < nv) {
-            const u32x4 x = zero ? u32x4{0, 0, 0, 0} : load_vec(row + v * N);
-            float f[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = value(Vec<T>::get(x, i), v * N + i);
-            store_vec(g + v * N, Vec<T>::pack(f));
-        } else {
-            const int64_t j = nv * N + (v - nv);  // the tail's elements take the threads behind the last vector
-            if (j < vocab) g[j] = Vec<T>::round(value(zero ? 0.0f : Vec<T>::one(row[j]), j));
-        }
+        x[u] = u32x4{0, 0, 0, 0};
+        if (!zero && v0 + u * kGradThreads + tid < nv) x[u] = load_at(row, v0 + u * kGradThreads);
     }
+    auto write = [&](auto nt) {
+#pragma unroll
+        for (int u = 0; u < kGradU; ++u) {
+            const int v = v0 + u * kGradThreads + tid;
+            if (v < nv) {
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = value(Vec<T>::get(x[u], i), (int64_t)v * N + i);
+                store_at<decltype(nt)::value>(g, v0 + u * kGradThreads, Vec<T>::pack(f));
+            } else {
+                const int64_t j = (int64_t)nv * N + (v - nv);  // the tail's elements take the threads behind the last vector
+                if (j < vocab) g[j] = Vec<T>::round(value(zero ? 0.0f : Vec<T>::one(row[j]), j));
+            }
+        }
+    };
+    if (whole_units(g))
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 // ------------------------------------------------------------------ distillation
 
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float* part) {
+__device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = part[0];
-    for (int w = 1; w < THREADS / 64; ++w) v += part[w];
-    __syncthreads();
     return v;
 }
 
-template <int THREADS>
-__device__ __forceinline__ float block_max(float v, float* part) {
+__device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = part[0];
-    for (int w = 1; w < THREADS / 64; ++w) v = fmaxf(v, part[w]);
-    __syncthreads();
     return v;
 }
 
@@ -621,79 +676,129 @@ __device__ __forceinline__ void fill_row(T* g, int64_t vocab, float f) {
     if (tail < vocab) g[tail] = Vec<T>::round(f);
 }
 
+constexpr int kSlots = 2 * ZS_DISTILL_MAX_K;  // of the table that finds equal ids
+
 struct DistillShared {
-    float q[ZS_DISTILL_MAX_K];  // the teacher's distribution
-    float x[ZS_DISTILL_MAX_K];  // the student's logits at its tokens
-    int32_t id[ZS_DISTILL_MAX_K];
-    float fpart[16];
+    float t[ZS_DISTILL_MAX_K];     // the teacher's logits, -infinity for unused entries
+    float x[ZS_DISTILL_MAX_K];     // the student's logits at its tokens
+    int32_t id[ZS_DISTILL_MAX_K];  // its tokens, -1 for unused entries
+    int32_t slot[kSlots];
+    int32_t repeated;
     Running part[16];
 };
 
-enum TeacherRow { kTeacherUsed, kTeacherEmpty, kTeacherBad };
+// The teacher's side of a row: its largest logit, 1 / the sum of its
+// exponentials and the log of that sum. Taken from shared memory by every wave
+// for itself, which costs less than a barrier.
+struct TeacherStats {
+    float max, inv, logsum;
+    bool bad;  // an id past the vocabulary, a NaN or +infinity
+};
 
-// The teacher's entries of a row into shared memory (sh.q holds its logits, of
-// unused entries -infinity), its largest logit and the log of the sum of its
-// exponentials.
-template <typename T, int THREADS>
-__device__ __forceinline__ TeacherRow teacher_row(const T* row, int64_t vocab, const Teacher& te, int64_t r, float k,
-                                                  DistillShared& sh, float* tmax_out, float* logq_out) {
-    const int32_t* ids = te.ids + r * te.k;
-    const float* tl = te.logits + r * te.k;
-    float tmax = -kInf, bad = 0.0f;
-    for (int i = threadIdx.x; i < te.k; i += THREADS) {
-        const int32_t j = ids[i];
-        const float t = j < 0 ? -kInf : tl[i];
-        sh.id[i] = j;
-        sh.q[i] = t;
-        sh.x[i] = j >= 0 && j < vocab ? Vec<T>::one(row[j]) : 0.0f;
-        tmax = fmaxf(tmax, t);
-        if (j >= vocab || !(t < kInf)) bad = 1.0f;
+__device__ __forceinline__ TeacherStats teacher_stats(int n, int64_t vocab, float k, const DistillShared& sh) {
+    const int lane = threadIdx.x & 63;
+    float m = -kInf;
+    bool bad = false;
+    for (int i = lane; i < n; i += 64) {
+        m = fmaxf(m, sh.t[i]);
+        bad = bad || sh.id[i] >= vocab || !(sh.t[i] < kInf);
     }
-    tmax = block_max<THREADS>(tmax, sh.fpart);
-    bad = block_max<THREADS>(bad, sh.fpart);
-    if (bad != 0.0f) return kTeacherBad;
-    if (tmax == -kInf) return kTeacherEmpty;
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < te.k; i += THREADS) sum += exp2f((sh.q[i] - tmax) * k);
-    sum = block_sum<THREADS>(sum, sh.fpart);
-    *tmax_out = tmax;
-    *logq_out = logf(sum);
-    return kTeacherUsed;
+    m = wave_max(m);
+    float s = 0.0f;
+    for (int i = lane; i < n; i += 64) s += exp2f((sh.t[i] - base_of(m)) * k);
+    s = wave_sum(s);
+    return TeacherStats{m, 1.0f / s, logf(s), (bool)__any(bad)};
 }
 
-// loss / T^2 = sum of q ((t - tmax) / T - (x - m) / T + log s - log sum of the
-// teacher's exponentials); sh.q turns from the teacher's logits into q.
-template <int THREADS>
-__device__ __forceinline__ float teacher_loss(int n, float tmax, float logq, float m, float logsum, float inv_t,
-                                              float k, DistillShared& sh) {
+// loss / T^2 = sum of q ((t - max) / T - (x - m) / T + log s - log sum of the
+// teacher's exponentials); one wave.
+__device__ __forceinline__ float teacher_loss(int n, const TeacherStats& ts, float m, float logsum, float inv_t,
+                                              float k, const DistillShared& sh) {
     float l = 0.0f;
-    const float inv = exp2f(-logq * (1.0f / kLn2));
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-        const float dt = sh.q[i] - tmax;
-        const float q = exp2f(dt * k) * inv;
-        sh.q[i] = q;
-        if (q > 0.0f) l += q * ((dt - (sh.x[i] - m)) * inv_t + (logsum - logq));
+    for (int i = threadIdx.x & 63; i < n; i += 64) {
+        const float dt = sh.t[i] - ts.max;
+        const float q = exp2f(dt * k) * ts.inv;
+        if (q > 0.0f) l += q * ((dt - (sh.x[i] - m)) * inv_t + (logsum - ts.logsum));
     }
-    return block_sum<THREADS>(l, sh.fpart);
+    return wave_sum(l);
+}
+
+// Marks sh.repeated where an id occurs twice: every used id goes into the first
+// free slot from its own on (sh.slot is -1 everywhere, and twice as long as
+// there can be ids).
+template <int THREADS>
+__device__ __forceinline__ void find_repeated(int n, DistillShared& sh) {
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const int id = sh.id[i];
+        if (id < 0) continue;
+        unsigned at = ((unsigned)id * 2654435761u) >> 21;
+        static_assert(kSlots == 1 << 11, "11 bits");
+        for (int tries = 0; tries < kSlots; ++tries) {
+            const int old = atomicCAS(&sh.slot[at], -1, id);
+            if (old == -1) break;
+            if (old == id) {
+                sh.repeated = 1;
+                break;
+            }
+            at = (at + 1) % kSlots;
+        }
+    }
 }
 
 // The entries' tokens are written again with the teacher's share, once for each
 // token by the first of its entries. p(x): the student's share of the
-// gradient. Behind a barrier after the row's gradient.
+// gradient. Behind a barrier after the row's gradient and find_repeated.
 template <typename T, int THREADS, typename P>
-__device__ __forceinline__ void teacher_gradient(int n, float scale, T* g, const DistillShared& sh, P p) {
+__device__ __forceinline__ void teacher_gradient(int n, const TeacherStats& ts, float k, float scale, T* g,
+                                                 const DistillShared& sh, P p) {
+    const bool repeated = sh.repeated != 0;
     for (int i = threadIdx.x; i < n; i += THREADS) {
-        if (!(sh.q[i] > 0.0f)) continue;
         const int id = sh.id[i];
-        float q = 0.0f;
-        bool first = true;
-        for (int j = 0; j < n; ++j) {
-            const bool same = sh.id[j] == id && sh.q[j] > 0.0f;
-            if (same) q += sh.q[j];
-            first = first && !(same && j < i);
+        if (id < 0) continue;
+        float q = exp2f((sh.t[i] - ts.max) * k);
+        if (repeated) {
+            q = 0.0f;
+            bool first = true;
+            for (int j = 0; j < n; ++j) {
+                if (sh.id[j] != id) continue;
+                first = first && j >= i;
+                q += exp2f((sh.t[j] - ts.max) * k);
+            }
+            if (!first) continue;
         }
-        if (first) g[id] = Vec<T>::round(p(sh.x[i]) - scale * q);
+        g[id] = Vec<T>::round(p(sh.x[i]) - scale * (q * ts.inv));
     }
+}
+
+// g = p(row) over the row's whole vectors, a group's loads ahead of its
+// arithmetic; g may be row.
+template <typename T, int THREADS, bool NT, typename P>
+__device__ __forceinline__ void map_row_as(const T* row, T* g, int nv, P p) {
+    constexpr int N = Vec<T>::kN;
+    constexpr int U = 4;
+    const int tid = threadIdx.x;
+    for (int v = 0; v < nv; v += U * THREADS) {
+        u32x4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * THREADS + tid < nv) x[u] = load_at(row, v + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (v + u * THREADS + tid >= nv) break;
+            float o[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[u], j));
+            store_at<NT>(g, v + u * THREADS, Vec<T>::pack(o));
+        }
+    }
+}
+
+template <typename T, int THREADS, typename P>
+__device__ __forceinline__ void map_row(const T* row, T* g, int nv, P p) {
+    if (whole_units(g))
+        map_row_as<T, THREADS, true>(row, g, nv, p);
+    else
+        map_row_as<T, THREADS, false>(row, g, nv, p);
 }
 
 // One block per row. NV > 0: the row's vectors are held in registers (up to NV
@@ -715,26 +820,41 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
         if (grad) fill_row(g, vocab, 0.0f);
         return;
     }
-    const int64_t nv = vocab / N;
-    const int64_t tail = nv * N + threadIdx.x;
+    const int nv = (int)(vocab / N), tid = threadIdx.x;
+    const int tail = nv * N + tid;
+    const int n = te.k;
+    // The teacher's entries, an entry a thread (more threads than entries, or
+    // up to 4 a thread), asked for before the row and put down behind it.
+    const int32_t* ids = te.ids + r * n;
+    const float* tl = te.logits + r * n;
+    int32_t id = -1;
+    float t = -kInf, z = 0.0f;
+    if ((int)threadIdx.x < n) {
+        id = ids[threadIdx.x];
+        t = tl[threadIdx.x];
+    }
     constexpr int kHeld = NV > 0 ? NV : 1;
     u32x4 x[kHeld];
     if (NV > 0) {
         const uint32_t none = Vec<T>::kNegInf;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t v = threadIdx.x + i * THREADS;
-            x[i] = v < nv ? load_vec(row + v * N) : u32x4{none, none, none, none};
+            x[i] = u32x4{none, none, none, none};
+            if (i * THREADS + tid < nv) x[i] = load_at(row, i * THREADS);
         }
     }
-    float tmax, logq;
-    const TeacherRow kind = teacher_row<T, THREADS>(row, vocab, te, r, k, sh, &tmax, &logq);
-    if (kind != kTeacherUsed) {
-        const float f = kind == kTeacherBad ? quiet_nan() : 0.0f;
-        if (threadIdx.x == 0) loss[r] = f;
-        if (grad) fill_row(g, vocab, f);
-        return;
-    }
+    if (grad)
+        for (int i = threadIdx.x; i < kSlots; i += THREADS) sh.slot[i] = -1;
+    if (threadIdx.x == 0) sh.repeated = 0;
+    auto put = [&](int i, int32_t id_i, float t_i, float x_i) {
+        sh.id[i] = id_i < 0 ? -1 : id_i;
+        sh.t[i] = id_i < 0 ? -kInf : t_i;
+        sh.x[i] = x_i;
+    };
+    auto at = [&](int32_t j) { return j >= 0 && j < vocab ? Vec<T>::one(row[j]) : 0.0f; };
+    if ((int)threadIdx.x < n) z = at(id);
+    if (n > THREADS)
+        for (int i = threadIdx.x + THREADS; i < n; i += THREADS) put(i, ids[i], tl[i], at(ids[i]));
     Fast f{-kInf, 0.0f, 0.0f, 0.0f};
     if (NV > 0) {
         constexpr int U = NV % 4 == 0 ? 4 : 1;
@@ -750,59 +870,65 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     } else {
         f = fast_running<T, THREADS, false>(row, vocab, k);
     }
-    f = fast_block_merge<THREADS, false>(f, k, reinterpret_cast<Fast*>(sh.part));
+    if ((int)threadIdx.x < n) put(threadIdx.x, id, t, z);
+    f = fast_block_merge<THREADS, false>(f, k, reinterpret_cast<Fast*>(sh.part));  // its barrier publishes the entries
+    const TeacherStats ts = teacher_stats(n, vocab, k, sh);
+    if (ts.bad || ts.max == -kInf) {
+        const float fill = ts.bad ? quiet_nan() : 0.0f;
+        if (threadIdx.x == 0) loss[r] = fill;
+        if (grad) fill_row(g, vocab, fill);
+        return;
+    }
     const float scale = w * temperature;
     if (ordinary(f)) {
-        const float l = teacher_loss<THREADS>(te.k, tmax, logq, f.m,
-                                              logf(f.s) - kLn2 * __builtin_fmaf(f.m, k, -f.c), inv_t, k, sh);
-        if (threadIdx.x == 0) loss[r] = w * temperature * temperature * l;
+        if (threadIdx.x < 64) {
+            const float l = teacher_loss(n, ts, f.m, logf(f.s) - kLn2 * __builtin_fmaf(f.m, k, -f.c), inv_t, k, sh);
+            if (threadIdx.x == 0) loss[r] = w * temperature * temperature * l;
+        }
         if (!grad) return;
+        find_repeated<THREADS>(n, sh);
         const float c = scale / f.s;
         auto p = [&](float z) { return c * exp2_raw(__builtin_fmaf(z, k, -f.c)); };
         if (NV > 0) {
+            auto write = [&](auto nt) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t v = threadIdx.x + i * THREADS;
-                float o[N];
-                asm("" : "+v"(x[i]));  // unpacked again here: the first pass's fp32 values are not kept
+                for (int i = 0; i < NV; ++i) {
+                    float o[N];
+                    asm("" : "+v"(x[i]));  // unpacked again here: the first pass's fp32 values are not kept
 #pragma unroll
-                for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[i], j));
-                if (v < nv) store_vec(g + v * N, Vec<T>::pack(o));
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                    for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[i], j));
+                    if (i * THREADS + tid < nv) store_at<decltype(nt)::value>(g, i * THREADS, Vec<T>::pack(o));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            if (whole_units(g))
+                write(std::true_type{});
+            else
+                write(std::false_type{});
         } else {
-            for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
-                const u32x4 y = load_vec(row + v * N);
-                float o[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(y, j));
-                store_vec(g + v * N, Vec<T>::pack(o));
-            }
+            map_row<T, THREADS>(row, g, nv, p);
         }
         if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
         __syncthreads();
-        teacher_gradient<T, THREADS>(te.k, scale, g, sh, p);
+        teacher_gradient<T, THREADS>(n, ts, k, scale, g, sh, p);
         return;
     }
     // any other row: differences from the maximum first, the row read again
     __syncthreads();
     const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, sh.part);
     const float m = base_of(a.m);
-    const float l = teacher_loss<THREADS>(te.k, tmax, logq, m, logf(a.s), inv_t, k, sh);
-    if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf && a.s == 0.0f ? kInf : l);
+    if (threadIdx.x < 64) {
+        const float l = teacher_loss(n, ts, m, logf(a.s), inv_t, k, sh);
+        if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf && a.s == 0.0f ? kInf : l);
+    }
     if (!grad) return;
+    find_repeated<THREADS>(n, sh);
     const float c = a.s == 0.0f ? 0.0f : scale / a.s;
     auto p = [&](float z) { return c * exp2f((z - m) * k); };
-    for (int64_t v = threadIdx.x; v < nv; v += THREADS) {
-        const u32x4 y = load_vec(row + v * N);
-        float o[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(y, j));
-        store_vec(g + v * N, Vec<T>::pack(o));
-    }
+    map_row<T, THREADS>(row, g, nv, p);
     if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
     __syncthreads();
-    teacher_gradient<T, THREADS>(te.k, scale, g, sh, p);
+    teacher_gradient<T, THREADS>(n, ts, k, scale, g, sh, p);
 }
 
 }  // namespace
@@ -827,13 +953,16 @@ void run_logprobs(Rows logits, int64_t rows, int64_t vocab, const int32_t* token
 int launch_logprobs(Rows logits, int dtype, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
                     const LogprobsOut& out, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    const bool few = rows <= 512 && vocab > 4096;
-    if (dtype == ZS_DTYPE_BF16 && few)
-        run_logprobs<uint16_t, 1024>(logits, rows, vocab, tokens, temperature, out, s);
+    // 512 threads a row where rows are few or long, else 256 (bf16, 8
+    // alternatives: 4096 x 128256 197 us against 227, 512 x 128256 31 against
+    // 33; 4096 x 65536 114 against 127 the other way round)
+    const bool wide = vocab > 8192 && (rows <= 1024 || vocab >= 98304);
+    if (dtype == ZS_DTYPE_BF16 && wide)
+        run_logprobs<uint16_t, 512>(logits, rows, vocab, tokens, temperature, out, s);
     else if (dtype == ZS_DTYPE_BF16)
         run_logprobs<uint16_t, 256>(logits, rows, vocab, tokens, temperature, out, s);
-    else if (few)
-        run_logprobs<float, 1024>(logits, rows, vocab, tokens, temperature, out, s);
+    else if (wide)
+        run_logprobs<float, 512>(logits, rows, vocab, tokens, temperature, out, s);
     else
         run_logprobs<float, 256>(logits, rows, vocab, tokens, temperature, out, s);
     return (int)hipGetLastError();
