@@ -256,14 +256,13 @@ __device__ __forceinline__ void fast_add(Fast& r, const u32x4 (&x)[U], float k) 
     }
 }
 
-template <typename T, int THREADS, bool ENTROPY>
-__device__ __forceinline__ Fast fast_running(const T* row, int64_t vocab, float k) {
+// r and the row's vectors from `first` on, then its tail.
+template <typename T, int THREADS, bool ENTROPY, int U>
+__device__ __forceinline__ Fast fast_running(Fast r, const T* row, int first, int64_t vocab, float k) {
     constexpr int N = Vec<T>::kN;
-    constexpr int U = 4;
     const int nv = (int)(vocab / N), tid = threadIdx.x;
     const uint32_t none = Vec<T>::kNegInf;
-    Fast r{-kInf, 0.0f, 0.0f, 0.0f};
-    int v = 0;  // of the block's first thread
+    int v = first;  // of the block's first thread
     u32x4 x[U];
     if (v + U * THREADS <= nv) {  // whole groups, the next one's loads ahead of each group's arithmetic
 #pragma unroll
@@ -331,7 +330,7 @@ template <typename T, int THREADS, bool ENTROPY>
 __device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float k, Running* part) {
     static_assert(sizeof(Fast) * (THREADS / 64) <= 1024, "part");
     Fast* fpart = reinterpret_cast<Fast*>(part);
-    const Fast own = fast_running<T, THREADS, ENTROPY>(row, vocab, k);
+    const Fast own = fast_running<T, THREADS, ENTROPY, 4>(Fast{-kInf, 0.0f, 0.0f, 0.0f}, row, 0, vocab, k);
     const Fast r = fast_block_merge<THREADS, ENTROPY>(own, k, fpart);
     if (ordinary(r)) {
         // from c to the maximum: x k - c = (x - m) k + (m k - c)
@@ -440,7 +439,7 @@ struct TopShared {
     float group[64];
     float x[kListed];
     int id[kListed];
-    int owner[512];
+    int owner[1024];
     int n, owners;
 };
 
@@ -622,20 +621,17 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
         return (hot - p * (gl + gh * (fmaxf(l, kLowest) + h))) * inv_t;
     };
     const int v0 = (int)tile * (kGradThreads * kGradU);
-    u32x4 x[kGradU];
-#pragma unroll
-    for (int u = 0; u < kGradU; ++u) {
-        x[u] = u32x4{0, 0, 0, 0};
-        if (!zero && v0 + u * kGradThreads + tid < nv) x[u] = load_at(row, v0 + u * kGradThreads);
-    }
+    // vector by vector: with more loads in flight a thread, reads and writes
+    // disturb each other more (4096 x 128256 bf16 398 us against 363)
     auto write = [&](auto nt) {
 #pragma unroll
         for (int u = 0; u < kGradU; ++u) {
             const int v = v0 + u * kGradThreads + tid;
             if (v < nv) {
+                const u32x4 x = zero ? u32x4{0, 0, 0, 0} : load_at(row, v0 + u * kGradThreads);
                 float f[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = value(Vec<T>::get(x[u], i), (int64_t)v * N + i);
+                for (int i = 0; i < N; ++i) f[i] = value(Vec<T>::get(x, i), (int64_t)v * N + i);
                 store_at<decltype(nt)::value>(g, v0 + u * kGradThreads, Vec<T>::pack(f));
             } else {
                 const int64_t j = (int64_t)nv * N + (v - nv);  // the tail's elements take the threads behind the last vector
@@ -770,14 +766,14 @@ __device__ __forceinline__ void teacher_gradient(int n, const TeacherStats& ts, 
     }
 }
 
-// g = p(row) over the row's whole vectors, a group's loads ahead of its
+// g = p(row) over the row's whole vectors from `first` on, a group's loads ahead of its
 // arithmetic; g may be row.
 template <typename T, int THREADS, bool NT, typename P>
-__device__ __forceinline__ void map_row_as(const T* row, T* g, int nv, P p) {
+__device__ __forceinline__ void map_row_as(const T* row, T* g, int first, int nv, P p) {
     constexpr int N = Vec<T>::kN;
     constexpr int U = 4;
     const int tid = threadIdx.x;
-    for (int v = 0; v < nv; v += U * THREADS) {
+    for (int v = first; v < nv; v += U * THREADS) {
         u32x4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -794,17 +790,18 @@ __device__ __forceinline__ void map_row_as(const T* row, T* g, int nv, P p) {
 }
 
 template <typename T, int THREADS, typename P>
-__device__ __forceinline__ void map_row(const T* row, T* g, int nv, P p) {
+__device__ __forceinline__ void map_row(const T* row, T* g, int first, int nv, P p) {
+    if (first >= nv) return;
     if (whole_units(g))
-        map_row_as<T, THREADS, true>(row, g, nv, p);
+        map_row_as<T, THREADS, true>(row, g, first, nv, p);
     else
-        map_row_as<T, THREADS, false>(row, g, nv, p);
+        map_row_as<T, THREADS, false>(row, g, first, nv, p);
 }
 
-// One block per row. NV > 0: the row's vectors are held in registers (up to NV
-// a thread) between the pass that sums their exponentials as they arrive and
-// the pass that writes the gradient, so logits are read once; 0: the second
-// pass reads them again.
+// One block per row. The row's first vectors, NV a thread, are held in registers
+// between the pass that sums their exponentials as they arrive and the pass
+// that writes the gradient, so they are read once; what lies behind them (in
+// rows longer than a compute unit's registers hold) is read again.
 template <typename T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t stride, int64_t vocab, Teacher te,
                                                      float temperature, float inv_t, float k,
@@ -833,15 +830,12 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
         id = ids[threadIdx.x];
         t = tl[threadIdx.x];
     }
-    constexpr int kHeld = NV > 0 ? NV : 1;
-    u32x4 x[kHeld];
-    if (NV > 0) {
-        const uint32_t none = Vec<T>::kNegInf;
+    u32x4 x[NV];
+    const uint32_t none = Vec<T>::kNegInf;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i] = u32x4{none, none, none, none};
-            if (i * THREADS + tid < nv) x[i] = load_at(row, i * THREADS);
-        }
+    for (int i = 0; i < NV; ++i) {
+        x[i] = u32x4{none, none, none, none};
+        if (i * THREADS + tid < nv) x[i] = load_at(row, i * THREADS);
     }
     if (grad)
         for (int i = threadIdx.x; i < kSlots; i += THREADS) sh.slot[i] = -1;
@@ -856,20 +850,15 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     if (n > THREADS)
         for (int i = threadIdx.x + THREADS; i < n; i += THREADS) put(i, ids[i], tl[i], at(ids[i]));
     Fast f{-kInf, 0.0f, 0.0f, 0.0f};
-    if (NV > 0) {
-        constexpr int U = NV % 4 == 0 ? 4 : 1;
 #pragma unroll
-        for (int i = 0; i < NV; i += U) {
-            u32x4 y[U];
+    for (int i = 0; i < NV; i += 4) {
+        u32x4 y[4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) y[u] = x[i + u];
-            fast_add<T, false>(f, y, k);
-            __builtin_amdgcn_sched_barrier(0);  // the held vectors leave no registers for a second group in flight
-        }
-        if (tail < vocab) f = fast_merge<false>(f, fast_one(Vec<T>::one(row[tail]), k), k);
-    } else {
-        f = fast_running<T, THREADS, false>(row, vocab, k);
+        for (int u = 0; u < 4; ++u) y[u] = x[i + u];
+        fast_add<T, false>(f, y, k);
+        __builtin_amdgcn_sched_barrier(0);  // the held vectors leave no registers for a second group in flight
     }
+    f = fast_running<T, THREADS, false, NV >= 16 ? 2 : 4>(f, row, NV * THREADS, vocab, k);
     if ((int)threadIdx.x < n) put(threadIdx.x, id, t, z);
     f = fast_block_merge<THREADS, false>(f, k, reinterpret_cast<Fast*>(sh.part));  // its barrier publishes the entries
     const TeacherStats ts = teacher_stats(n, vocab, k, sh);
@@ -889,25 +878,22 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
         find_repeated<THREADS>(n, sh);
         const float c = scale / f.s;
         auto p = [&](float z) { return c * exp2_raw(__builtin_fmaf(z, k, -f.c)); };
-        if (NV > 0) {
-            auto write = [&](auto nt) {
+        auto write = [&](auto nt) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    float o[N];
-                    asm("" : "+v"(x[i]));  // unpacked again here: the first pass's fp32 values are not kept
+            for (int i = 0; i < NV; ++i) {
+                float o[N];
+                asm("" : "+v"(x[i]));  // unpacked again here: the first pass's fp32 values are not kept
 #pragma unroll
-                    for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[i], j));
-                    if (i * THREADS + tid < nv) store_at<decltype(nt)::value>(g, i * THREADS, Vec<T>::pack(o));
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            };
-            if (whole_units(g))
-                write(std::true_type{});
-            else
-                write(std::false_type{});
-        } else {
-            map_row<T, THREADS>(row, g, nv, p);
-        }
+                for (int j = 0; j < N; ++j) o[j] = p(Vec<T>::get(x[i], j));
+                if (i * THREADS + tid < nv) store_at<decltype(nt)::value>(g, i * THREADS, Vec<T>::pack(o));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (whole_units(g))
+            write(std::true_type{});
+        else
+            write(std::false_type{});
+        map_row<T, THREADS>(row, g, NV * THREADS, nv, p);
         if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
         __syncthreads();
         teacher_gradient<T, THREADS>(n, ts, k, scale, g, sh, p);
@@ -925,7 +911,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     find_repeated<THREADS>(n, sh);
     const float c = a.s == 0.0f ? 0.0f : scale / a.s;
     auto p = [&](float z) { return c * exp2f((z - m) * k); };
-    map_row<T, THREADS>(row, g, nv, p);
+    map_row<T, THREADS>(row, g, 0, nv, p);
     if (tail < vocab) g[tail] = Vec<T>::round(p(Vec<T>::one(row[tail])));
     __syncthreads();
     teacher_gradient<T, THREADS>(n, ts, k, scale, g, sh, p);
@@ -1008,19 +994,20 @@ void run_distill(Rows logits, int64_t rows, int64_t vocab, const Teacher& t, dou
 template <typename T>
 int pick_distill(Rows logits, int64_t rows, int64_t vocab, const Teacher& t, double temperature, float* loss,
                  void* grad, int64_t grad_stride, hipStream_t s) {
+    // As many threads and vectors a thread as hold the row; 20 vectors are what
+    // 1024 threads have registers for (4096 x 151936 bf16, 19 vectors: 487 us,
+    // read twice 549; 1024 x 151936 fp32, 20 of 38 held: 271 us against 330).
     const int64_t nv = vocab / Vec<T>::kN;  // 16-byte vectors of a row
     if (nv <= 256 * 4)
         run_distill<T, 256, 4>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
-    else if (nv <= 256 * 16)
-        run_distill<T, 256, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+    else if (nv <= 512 * 8)
+        run_distill<T, 512, 8>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
     else if (nv <= 512 * 16)
         run_distill<T, 512, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
     else if (nv <= 1024 * 16)
         run_distill<T, 1024, 16>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
-    else if (nv <= 1024 * 20)
-        run_distill<T, 1024, 20>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
     else
-        run_distill<T, 1024, 0>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
+        run_distill<T, 1024, 20>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);
     return (int)hipGetLastError();
 }
 
