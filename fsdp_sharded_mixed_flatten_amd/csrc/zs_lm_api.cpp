@@ -15,7 +15,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;
 // Largest weight matrix: a wave (64 work-items) a row in one launch, columns
 // counted in int32.
 constexpr int64_t kMaxOut = int64_t(1) << 25;
-constexpr int64_t kMaxIn = int64_t(1) << 30;
+constexpr int64_t kMaxIn = int64_t(1) << 29;
 // Largest row stride and matrix extent: byte addresses stay far inside int64.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
@@ -111,7 +111,7 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
     const zs::TensorEntry& t = plan->tensors[(size_t)tensor];
     if (out_features < 0 || in_features < 0 || out_features > kMaxOut || in_features > kMaxIn ||
         out_features * in_features != t.numel)
-        return report(ZS_EINVAL, "tensor %d has %lld elements, not %lld x %lld (at most 2^25 x 2^30)", tensor,
+        return report(ZS_EINVAL, "tensor %d has %lld elements, not %lld x %lld (at most 2^25 x 2^29)", tensor,
                       (long long)t.numel, (long long)out_features, (long long)in_features);
     if (rows < 0 || rows > ZS_QUANT_MATVEC_MAX_ROWS)
         return report(ZS_EINVAL, "rows = %d outside [0, %d]", rows, ZS_QUANT_MATVEC_MAX_ROWS);
@@ -131,7 +131,7 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
         if (zs_status st = check_apart(ys, span(codes_all, plan->T * bits / 8), "y", "codes_all")) return st;
         if (zs_status st = check_apart(ys, span(scales_all, 4 * n_scales * plan->world), "y", "scales_all")) return st;
     }
-    zs::QuantWeight w{codes_all,  scales_all, t.flat_off, out_features, in_features, plan->S, n_scales, bits, 0};
+    zs::QuantWeight w{codes_all,  scales_all, t.flat_off, out_features, in_features, plan->S, n_scales, plan->world, bits, 0};
     while ((1 << w.block_shift) < block) ++w.block_shift;
     zs::trace_call("zs_quant_matvec", plan, 0, t.flat_off, t.numel, stream);
     return zs::report_hip(zs::launch_quant_matvec(w, zs::Rows{x_bf16, x_stride}, rows, y, y_dtype, y_stride, stream),

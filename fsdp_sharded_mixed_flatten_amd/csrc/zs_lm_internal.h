@@ -33,6 +33,7 @@ struct QuantWeight {
     int64_t n_out, n_in;
     int64_t shard;     // S
     int64_t n_scales;  // scales a rank
+    int32_t world;     // N
     int32_t bits;
     int32_t block_shift;  // log2(block)
 };

@@ -42,6 +42,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // ------------------------------------------------------------------ any layout
+// Blocks of 8 and 16, rows of less than 32 columns and shards shorter than a row.
 // One wave per row of W and M rows of x. The wave walks the row in units of 8
 // elements of the flat buffer that start at multiples of 8: a unit never
 // crosses a shard (S is a multiple of 8) or a block (blocks start at multiples
@@ -162,6 +163,7 @@ void run_any(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 __attribute__((aligned(4))) f32x4_u4;
+typedef u32x4 __attribute__((aligned(4))) u32x4_u4;
 
 constexpr int kChunk = 128;
 
@@ -182,6 +184,9 @@ struct Codes<4> {
         w = u32x4{c[0], c[1], d[0], d[1]};
     }
     // The conversion takes a byte's low 4 bits as a signed value / 16.
+    __device__ __forceinline__ void set(const uint32_t* d) { w = u32x4{d[0], d[1], d[2], d[3]}; }
+    // Leaves out codes of word j (8 bits: of its halves).
+    __device__ __forceinline__ void keep(int j, uint32_t m, uint32_t) { w[j] &= m; }
     static constexpr float kUnit = 16.0f;
     static __device__ __forceinline__ float low(uint32_t d, int byte) {
         return __builtin_amdgcn_cvt_off_f32_i4((int)((d >> (8 * byte)) & 0xFFu));
@@ -219,6 +224,14 @@ struct Codes<8> {
             w[1][2 + h] = d[1];
         }
     }
+    __device__ __forceinline__ void set(const uint32_t* d) {
+        w[0] = u32x4{d[0], d[1], d[2], d[3]};
+        w[1] = u32x4{d[4], d[5], d[6], d[7]};
+    }
+    __device__ __forceinline__ void keep(int j, uint32_t m0, uint32_t m1) {
+        w[j / 2][2 * (j % 2)] &= m0;
+        w[j / 2][2 * (j % 2) + 1] &= m1;
+    }
     static constexpr float kUnit = 1.0f;
     __device__ __forceinline__ bf16x8 word(int j) const {
         u32x4 v;
@@ -232,27 +245,42 @@ struct Codes<8> {
     }
 };
 
-// What a wave loads of W for one span.
-template <int BITS, int SHIFT, int SPAN>
+// What a wave loads of W for one span of columns, whole blocks.
+template <int BITS, int SHIFT, int SPAN_>
 struct Span {
+    static constexpr int SPAN = SPAN_, kBits = BITS;
     static constexpr int NB = SHIFT >= 7 ? 1 : kChunk >> SHIFT;  // blocks a chunk (1: a block is a chunk or two)
     static constexpr int kScales = SPAN * kChunk >= 1 << SHIFT ? SPAN * kChunk >> SHIFT : 1;
+    static constexpr int kBeyond = 0;       // columns behind a span that its loads may touch
+    static constexpr bool kRagged = false;  // rows may end inside 8 columns
     Codes<BITS> c[SPAN];
     float s[kScales];
+
+    // The codes and scales of the row of W that this lane loads, from its column
+    // 32 g on. Rows behind the last one repeat it and are not stored.
+    struct Row {
+        const char* code;
+        const float* scale;
+        __device__ __forceinline__ Row(const QuantWeight& w, int64_t o, int g) {
+            const int64_t j = w.off + (o < w.n_out ? o : w.n_out - 1) * w.n_in;
+            code = static_cast<const char*>(w.codes) + (j + 32 * g) * BITS / 8;
+            scale = w.scales + (j >> SHIFT);
+        }
+    };
 
     // The span of columns from k0. TAIL: it may reach past the row's end, where
     // codes and scales count as zero.
     template <bool TAIL>
-    __device__ __forceinline__ void load(const char* code, const float* scale, int k0, int n_in, int g) {
+    __device__ __forceinline__ void load(const Row& row, int k0, int n_in, int g) {
 #pragma unroll
         for (int p = 0; p < SPAN; ++p) {
             const int k = k0 + p * kChunk;
             if (!TAIL || k + 32 * g < n_in)
-                c[p].load(code + (int64_t)k * BITS / 8);
+                c[p].load(row.code + (int64_t)k * BITS / 8);
             else
                 c[p].zero();
         }
-        const float* sp = scale + (k0 >> SHIFT);
+        const float* sp = row.scale + (k0 >> SHIFT);
         if (TAIL) {
 #pragma unroll
             for (int i = 0; i < kScales; ++i) s[i] = k0 + (i << SHIFT) < n_in ? sp[i] : 0.0f;
@@ -299,14 +327,160 @@ struct Span {
     static constexpr int kUnitJ = NB == 1 ? 1 : 4, kUnitG = NB == 1 ? 4 : 1;
 };
 
-// The codes and scales of the row of W that this lane loads, from its column
-// 32 g on. Rows behind the last one repeat it and are not stored.
-template <int BITS, int SHIFT>
-__device__ __forceinline__ void row_of(const QuantWeight& w, int64_t o, int g, const char** code,
-                                       const float** scale) {
-    const int64_t j = w.off + (o < w.n_out ? o : w.n_out - 1) * w.n_in;
-    *code = static_cast<const char*>(w.codes) + (j + 32 * g) * BITS / 8;
-    *scale = w.scales + (j >> SHIFT);
+// ------------------------------------------------------------------ split blocks
+// What a wave loads of W for one span where blocks of 32 or more elements start
+// anywhere in a row: tensor offset, n_in or S are no multiples of block. A
+// window of 32 columns then holds parts of at most two blocks, A before and B
+// behind a boundary, and is multiplied twice, with the codes of B and then those
+// of A left out: two partial sums, each with its own scale. Where a shard's
+// last block is shorter than 32, the window around it holds a third, C. Scales
+// follow one another from boundary to boundary, also from one shard to the next.
+//
+// A row's first code may lie at any 4 or 8 bits: a lane loads the words around
+// its 32 codes and shifts them into place. Lane (g, r) works out boundary and
+// scales of row r in window g of a chunk; the other lane groups ask it for them.
+// More than twice the arithmetic and loads of whole blocks, which bound it: 8191
+// x 8191 int4, blocks of 128, takes 26 us with one row of x and 39 with 16 (8192
+// x 8192 in whole blocks 12 and 16; k_matvec_any 26 and 174).
+template <int BITS, int SPAN_>
+struct SplitSpan {
+    static constexpr int SPAN = SPAN_, kBits = BITS;
+    static constexpr int kWords = BITS;        // 32-bit words of 32 codes
+    static constexpr int kPer = 32 / BITS;     // codes a word
+    static constexpr int kBeyond = kPer;       // the word behind the lane's codes
+    static constexpr bool kRagged = true;
+    Codes<BITS> c[SPAN];
+    float sa[SPAN], sb[SPAN], sc[SPAN];
+    int edge[SPAN], edge2[SPAN];  // columns of the lane's window before the boundaries (32 and more: all)
+
+    struct Row {
+        const uint32_t* word;  // the one that holds the lane's first code
+        const uint32_t* end;   // of the payload's codes
+        int shift;             // of that code in its word, in bits
+        const float* scale;    // of the row's first element
+        int first;             // of the row's first element in its block
+        int left;              // elements of the row's first shard from there on (or more than the row has)
+        int log2_block;
+        __device__ __forceinline__ Row(const QuantWeight& w, int64_t o, int g) {
+            const int64_t j = w.off + (o < w.n_out ? o : w.n_out - 1) * w.n_in;
+            const int64_t jg = j + 32 * g, q = j / w.shard, s = j - q * w.shard;
+            const uint32_t* words = static_cast<const uint32_t*>(w.codes);
+            word = words + jg / kPer;
+            end = words + w.shard * w.world / kPer;
+            shift = (int)(jg % kPer) * BITS;
+            log2_block = w.block_shift;
+            scale = w.scales + q * w.n_scales + (s >> log2_block);
+            first = (int)(s & ((1 << log2_block) - 1));
+            const int64_t rest = w.shard - s;
+            left = rest < w.n_in ? (int)rest : INT32_MAX / 2;
+        }
+    };
+
+    template <bool TAIL>
+    __device__ __forceinline__ void load(const Row& row, int k0, int n_in, int g) {
+#pragma unroll
+        for (int p = 0; p < SPAN; ++p) {
+            const int k = k0 + p * kChunk, kg = k + 32 * g;
+            const uint32_t* at = row.word + k / kPer;
+            uint32_t d[kWords + 1];
+            if (!TAIL) {
+#pragma unroll
+                for (int i = 0; i < kWords; i += 4) {
+                    const u32x4 v = *reinterpret_cast<const u32x4_u4*>(at + i);
+                    d[i] = v[0], d[i + 1] = v[1], d[i + 2] = v[2], d[i + 3] = v[3];
+                }
+                d[kWords] = at[kWords];
+            } else {
+                const int used = n_in - kg;  // codes from the lane's first column on
+#pragma unroll
+                for (int i = 0; i <= kWords; ++i) d[i] = (i - 1) * kPer < used && at + i < row.end ? at[i] : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                d[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], row.shift);
+                if (TAIL) d[i] &= mask(n_in - kg - i * kPer);
+            }
+            c[p].set(d);
+            // boundary and scales of window g
+            int index, next;
+            if (kg < row.left) {
+                index = (row.first + kg) >> row.log2_block;
+                next = ((index + 1) << row.log2_block) - row.first;
+                next = next < row.left ? next : row.left;
+            } else {
+                const int b = (kg - row.left) >> row.log2_block;
+                index = ((row.first + row.left - 1) >> row.log2_block) + 1 + b;
+                next = ((b + 1) << row.log2_block) + row.left;
+            }
+            edge[p] = next - kg;
+            sa[p] = !TAIL || kg < n_in ? row.scale[index] : 0.0f;
+            sb[p] = next < n_in && edge[p] < 32 ? row.scale[index + 1] : 0.0f;
+            int last = next + (1 << row.log2_block);
+            if (next < row.left && last > row.left) last = row.left;
+            edge2[p] = last - kg;
+            sc[p] = last < n_in && edge2[p] < 32 ? row.scale[index + 2] : 0.0f;
+        }
+    }
+
+    // The first n codes of a word.
+    static __device__ __forceinline__ uint32_t mask(int n) {
+        return n >= kPer ? ~0u : n <= 0 ? 0u : (1u << (n * BITS)) - 1u;
+    }
+
+    template <int MT, int NI>
+    __device__ __forceinline__ void multiply(int p, const u32x4 (&xv)[MT][4], f32x4 (&acc)[MT]) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+        c[p].transpose();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int from = 16 * j + r;
+            const int n = __shfl(edge[p], from, 64) - 8 * g;  // this lane's codes of window j before the boundary
+            auto part = [&](const Codes<BITS>& codes, float scale) {
+                const bf16x8 cv = codes.word(j);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const f32x4 v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[m][j]), cv,
+                                                                            zero, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) acc[m][i] = __builtin_fmaf(v[i], scale, acc[m][i]);
+                }
+            };
+            const float a = __shfl(sa[p], from, 64);
+            if (__all(n >= 8)) {  // no row has a boundary in this window
+                part(c[p], a);
+                continue;
+            }
+            Codes<BITS> before = c[p], behind = c[p];
+            before.keep(j, mask(n), mask(n - kPer));
+            behind.keep(j, ~mask(n), ~mask(n - kPer));
+            part(before, a);
+            const int n2 = __shfl(edge2[p], from, 64) - 8 * g;
+            if (__any(n2 < 8)) {
+                Codes<BITS> third = behind;
+                behind.keep(j, mask(n2), mask(n2 - kPer));
+                third.keep(j, ~mask(n2), ~mask(n2 - kPer));
+                part(third, __shfl(sc[p], from, 64));
+            }
+            part(behind, __shfl(sb[p], from, 64));
+        }
+    }
+    static constexpr int kUnitJ = 4, kUnitG = 1;
+};
+
+// 8 columns of a row of x from k on, zero from the row's end; RAGGED: the row
+// may end inside them.
+template <bool RAGGED>
+__device__ __forceinline__ u32x4 load_x(const uint16_t* x, int k, int n_in) {
+    u32x4 v = u32x4{0, 0, 0, 0};
+    if (k + 8 <= n_in || (!RAGGED && k < n_in)) {
+        v = *reinterpret_cast<const u32x4_u2*>(x + k);
+    } else if (RAGGED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < n_in) v[i >> 1] |= (uint32_t)x[k + i] << (16 * (i & 1));
+    }
+    return v;
 }
 
 // Up to 4 rows of x, ROWS of them through shared memory: a wave loads its
@@ -318,10 +492,10 @@ __device__ __forceinline__ void row_of(const QuantWeight& w, int64_t o, int g, c
 // Reads at 5.1 TB/s at 28672 x 8192 int4 (24.5 us, one row), 6.0 TB/s at 8192 x
 // 128256 int8 (180 us, 4 rows); bound by memory there and by latency in
 // products of a few MB (4096 x 4096 int4 4.6 us, an empty launch 1.6 us).
-template <int BITS, int SHIFT, int SPAN, int ROWS>
+template <typename S, int ROWS>
 __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_t* __restrict__ x, int64_t x_stride,
                                                     int rows, void* __restrict__ y, int y_bf16, int64_t y_stride) {
-    using S = Span<BITS, SHIFT, SPAN>;
+    constexpr int SPAN = S::SPAN;
     constexpr int kUnits = SPAN * kChunk / 8;  // 16-byte units of a row of x in a span: a lane each
     constexpr int kPitch = kUnits + 4;
     static_assert(kUnits <= 64, "a wave loads a row of x at once");
@@ -330,9 +504,7 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
     const int g = lane >> 4, r = lane & 15;
     const int64_t o = (int64_t)blockIdx.x * 16 + r;
     const int n_in = (int)w.n_in;
-    const char* code;
-    const float* scale;
-    row_of<BITS, SHIFT>(w, o, g, &code, &scale);
+    const typename S::Row row(w, o, g);
     u32x4* const xs = shared + wave * (ROWS * kPitch);
     const int token = (r & 3) * 4 + (r >> 2);
     const u32x4* const xr = xs + (token < rows ? token : 0) * kPitch + S::kUnitG * g;
@@ -344,13 +516,17 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
     };
     auto load = [&](Loaded& b, int k0, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
-        b.s.template load<TAIL>(code, scale, k0, n_in, g);
+        b.s.template load<TAIL>(row, k0, n_in, g);
         const int k = k0 + 8 * lane;
 #pragma unroll
         for (int m = 0; m < ROWS; ++m) {
             b.x[m] = u32x4{0, 0, 0, 0};
-            if (m < rows && lane < kUnits && (!TAIL || k < n_in))
-                b.x[m] = *reinterpret_cast<const u32x4_u2*>(x + m * x_stride + k);
+            if (m < rows && lane < kUnits) {
+                if (TAIL)
+                    b.x[m] = load_x<S::kRagged>(x + m * x_stride, k, n_in);
+                else
+                    b.x[m] = *reinterpret_cast<const u32x4_u2*>(x + m * x_stride + k);
+            }
         }
     };
     auto compute = [&](Loaded& b, int k0, auto tail) {
@@ -375,27 +551,27 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
             b.s.template multiply<1, 1>(p, xv[p], acc);
         }
     };
-    // whole spans, then the row's last one if it is none
-    constexpr int kSpan = SPAN * kChunk;
+    // spans that lie in the row with all their loads touch, then the others
+    constexpr int kSpan = SPAN * kChunk, kWhole = kSpan + S::kBeyond;
     const int step = waves * kSpan;
     int k0 = wave * kSpan;
-    if (k0 + kSpan <= n_in) {
+    if (k0 + kWhole <= n_in) {
         Loaded a, b;
         load(a, k0, std::false_type{});
         while (true) {
-            const bool more = k0 + step + kSpan <= n_in;
+            const bool more = k0 + step + kWhole <= n_in;
             if (more) load(b, k0 + step, std::false_type{});
             compute(a, k0, std::false_type{});
             k0 += step;
             if (!more) break;
-            const bool again = k0 + step + kSpan <= n_in;
+            const bool again = k0 + step + kWhole <= n_in;
             if (again) load(a, k0 + step, std::false_type{});
             compute(b, k0, std::false_type{});
             k0 += step;
             if (!again) break;
         }
     }
-    if (k0 < n_in) {
+    for (; k0 < n_in; k0 += step) {
         Loaded a;
         load(a, k0, std::true_type{});
         compute(a, k0, std::true_type{});
@@ -407,7 +583,7 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
     if (wave > 0) return;
     float v = acc[0][0];
     for (int q = 1; q < waves; ++q) v += sums[(q - 1) * 64 + lane];
-    if (g < rows && o < w.n_out) store_y(y, y_bf16, g * y_stride + o, v * Codes<BITS>::kUnit);
+    if (g < rows && o < w.n_out) store_y(y, y_bf16, g * y_stride + o, v * Codes<S::kBits>::kUnit);
 }
 
 // 5 and more rows of x, in MT tiles of 16: what costs here is bringing x to the
@@ -418,11 +594,11 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
 // 28672 x 8192 int4 with 16 rows: 44 us against 76 with each wave loading its
 // own operands, 64 rows 118 against 258; at 2048 x 11008 with 16 rows 9.2
 // against 10.8.
-template <int BITS, int SHIFT, int MT, int SPAN, int RW, int KW>
+template <typename S, int MT, int RW, int KW>
 __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, const uint16_t* __restrict__ x,
                                                               int64_t x_stride, int rows, void* __restrict__ y,
                                                               int y_bf16, int64_t y_stride) {
-    using S = Span<BITS, SHIFT, SPAN>;
+    constexpr int SPAN = S::SPAN;
     constexpr int kSpan = SPAN * kChunk;
     constexpr int kUnits = kSpan / 8;           // 16-byte units of a row of x in a span
     constexpr int kPitch = kUnits + 1;          // rows start in different banks
@@ -438,9 +614,7 @@ __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, con
     const int64_t o = ((int64_t)blockIdx.x * RW + rw) * 16 + r;
     const int n_in = (int)w.n_in;
     const int turns = (n_in + KW * kSpan - 1) / (KW * kSpan);
-    const char* code;
-    const float* scale;
-    row_of<BITS, SHIFT>(w, o, g, &code, &scale);
+    const typename S::Row wrow(w, o, g);
     const int token = (r & 3) * 4 + (r >> 2);
     int xrow[MT];
 #pragma unroll
@@ -455,13 +629,12 @@ __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, con
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int u = rw * 64 + lane + i * (64 * RW), row = u / kUnits, k = k0 + u % kUnits * 8;
-            xn[i] = u32x4{0, 0, 0, 0};
-            if (row < rows && k < n_in) xn[i] = *reinterpret_cast<const u32x4_u2*>(x + row * x_stride + k);
+            xn[i] = row < rows ? load_x<S::kRagged>(x + row * x_stride, k, n_in) : u32x4{0, 0, 0, 0};
         }
-        if (k0 + kSpan <= n_in)
-            b.template load<false>(code, scale, k0, n_in, g);
+        if (k0 + kSpan + S::kBeyond <= n_in)
+            b.template load<false>(wrow, k0, n_in, g);
         else
-            b.template load<true>(code, scale, k0, n_in, g);
+            b.template load<true>(wrow, k0, n_in, g);
     };
     auto store = [&](int turn) {
         u32x4* to = xl + ((turn & 1) * KW + kw) * kTile;
@@ -522,7 +695,7 @@ __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 16 * m + 4 * i + g;
-            if (row < rows) store_y(y, y_bf16, row * y_stride + o, acc[m][i] * Codes<BITS>::kUnit);
+            if (row < rows) store_y(y, y_bf16, row * y_stride + o, acc[m][i] * Codes<S::kBits>::kUnit);
         }
 }
 
@@ -536,29 +709,29 @@ struct Product {
     hipStream_t s;
 };
 
-template <int BITS, int SHIFT, int ROWS>
+template <typename S, int ROWS>
 void run_few(const Product& a) {
-    constexpr int kSpanChunks = 4;
-    const int64_t tiles = (a.w.n_out + 15) / 16;
-    const int64_t spans = (a.w.n_in + kSpanChunks * kChunk - 1) / (kSpanChunks * kChunk);
+    constexpr int kSpan = S::SPAN * kChunk;
+    const int64_t tiles = (a.w.n_out + 15) / 16, spans = (a.w.n_in + kSpan - 1) / kSpan;
     // 8 waves a workgroup while a workgroup a CU is about all there is (4096 x
     // 4096 int4 4.8 us against 5.4 with 4), else 4 (28672 x 8192 int4 24.4 us
     // against 26.5 with 8, 8192 x 128256 114 against 147)
     const int most = tiles <= 256 ? 8 : 4;
     const int waves = spans < most ? (int)spans : most;
-    const size_t lds = (size_t)waves * ROWS * (kSpanChunks * kChunk / 8 + 4) * 16 + (size_t)(waves - 1) * 64 * 4;
-    hipLaunchKernelGGL((k_matvec_few<BITS, SHIFT, kSpanChunks, ROWS>), dim3((unsigned)tiles), dim3(64 * waves), lds,
-                       a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y, a.y_bf16, a.y_stride);
-}
-
-template <int BITS, int SHIFT, int MT, int SPAN, int RW, int KW>
-void run_rows(const Product& a) {
-    hipLaunchKernelGGL((k_matvec_rows<BITS, SHIFT, MT, SPAN, RW, KW>),
-                       dim3((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW))), dim3(64 * RW * KW), 0, a.s, a.w,
+    const size_t lds = (size_t)waves * ROWS * (kSpan / 8 + 4) * 16 + (size_t)(waves - 1) * 64 * 4;
+    hipLaunchKernelGGL((k_matvec_few<S, ROWS>), dim3((unsigned)tiles), dim3(64 * waves), lds, a.s, a.w,
                        static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y, a.y_bf16, a.y_stride);
 }
 
-template <int BITS, int SHIFT>
+template <typename S, int MT, int RW, int KW>
+void run_rows(const Product& a) {
+    hipLaunchKernelGGL((k_matvec_rows<S, MT, RW, KW>), dim3((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW))),
+                       dim3(64 * RW * KW), 0, a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y,
+                       a.y_bf16, a.y_stride);
+}
+
+// S<SPAN>: what loads W, in spans of SPAN chunks.
+template <template <int> class S>
 void run_block(const Product& a) {
     // Where 128 rows of W a workgroup still fill the chip, all 8 waves share x
     // (8192 x 128256 int4, 16 rows: 131 us against 192 with 4 groups of 4);
@@ -566,34 +739,47 @@ void run_block(const Product& a) {
     // against 68 with 2 groups of 4).
     const bool wide = a.w.n_out >= 128 * 256;
     if (a.rows == 1)
-        run_few<BITS, SHIFT, 1>(a);
+        run_few<S<4>, 1>(a);
     else if (a.rows <= 4)
-        run_few<BITS, SHIFT, 4>(a);
+        run_few<S<4>, 4>(a);
     else if (a.rows <= 16 && wide)
-        run_rows<BITS, SHIFT, 1, 4, 8, 1>(a);
+        run_rows<S<4>, 1, 8, 1>(a);
     else if (a.rows <= 16 && a.w.n_in > 2048)
-        run_rows<BITS, SHIFT, 1, 4, 2, 4>(a);
+        run_rows<S<4>, 1, 2, 4>(a);
     else if (a.rows <= 16)  // shorter spans where the long ones make one turn (2048 x 11008: 9.2 us against 11.6)
-        run_rows<BITS, SHIFT, 1, 2, 2, 4>(a);
+        run_rows<S<2>, 1, 2, 4>(a);
     else if (a.rows <= 32 && wide)
-        run_rows<BITS, SHIFT, 2, 2, 8, 1>(a);
+        run_rows<S<2>, 2, 8, 1>(a);
     else if (a.rows <= 32)
-        run_rows<BITS, SHIFT, 2, 2, 2, 4>(a);
+        run_rows<S<2>, 2, 2, 4>(a);
     else if (wide)
-        run_rows<BITS, SHIFT, 4, 1, 8, 1>(a);
+        run_rows<S<1>, 4, 8, 1>(a);
     else
-        run_rows<BITS, SHIFT, 4, 1, 2, 4>(a);
+        run_rows<S<1>, 4, 2, 4>(a);
 }
 
-template <int BITS>
-void run_blocks(const Product& a) {
-    switch (a.w.block_shift) {
-        case 5: return run_block<BITS, 5>(a);
-        case 6: return run_block<BITS, 6>(a);
-        case 7: return run_block<BITS, 7>(a);
-        default: return run_block<BITS, 8>(a);
-    }
-}
+template <int SPAN>
+using Whole4x32 = Span<4, 5, SPAN>;
+template <int SPAN>
+using Whole4x64 = Span<4, 6, SPAN>;
+template <int SPAN>
+using Whole4x128 = Span<4, 7, SPAN>;
+template <int SPAN>
+using Whole4x256 = Span<4, 8, SPAN>;
+template <int SPAN>
+using Whole8x32 = Span<8, 5, SPAN>;
+template <int SPAN>
+using Whole8x64 = Span<8, 6, SPAN>;
+template <int SPAN>
+using Whole8x128 = Span<8, 7, SPAN>;
+template <int SPAN>
+using Whole8x256 = Span<8, 8, SPAN>;
+// Two chunks a span at most: their boundaries and scales take registers too
+// (2049 x 60001 int4, one row: 46 us against 72 with 4; 16 rows 59 against 88).
+template <int SPAN>
+using Split4 = SplitSpan<4, (SPAN < 2 ? SPAN : 2)>;
+template <int SPAN>
+using Split8 = SplitSpan<8, (SPAN < 2 ? SPAN : 2)>;
 
 }  // namespace
 
@@ -601,15 +787,24 @@ int launch_quant_matvec(const QuantWeight& w, Rows x, int rows, void* y, int y_d
                         void* stream) {
     const Product a{w, x, rows, y, y_dtype == ZS_DTYPE_BF16, y_stride, (hipStream_t)stream};
     const int64_t block = int64_t(1) << w.block_shift;
-    const bool whole = block >= 32 && w.n_in > 0 && w.off % block == 0 && w.n_in % block == 0 && w.shard % block == 0;
-    if (whole && w.bits == 4)
-        run_blocks<4>(a);
-    else if (whole)
-        run_blocks<8>(a);
-    else if (w.bits == 4)
+    const bool four = w.bits == 4;
+    const bool whole = w.off % block == 0 && w.n_in % block == 0 && w.shard % block == 0;
+    // split blocks: at most one shard's end in a row
+    const bool split = w.shard >= w.n_in;
+    if (block >= 32 && w.n_in > 0 && whole) {
+        switch (w.block_shift) {
+            case 5: four ? run_block<Whole4x32>(a) : run_block<Whole8x32>(a); break;
+            case 6: four ? run_block<Whole4x64>(a) : run_block<Whole8x64>(a); break;
+            case 7: four ? run_block<Whole4x128>(a) : run_block<Whole8x128>(a); break;
+            default: four ? run_block<Whole4x256>(a) : run_block<Whole8x256>(a); break;
+        }
+    } else if (block >= 32 && w.n_in >= 32 && split) {
+        four ? run_block<Split4>(a) : run_block<Split8>(a);
+    } else if (four) {
         run_any<4>(w, x, rows, y, a.y_bf16, y_stride, a.s);
-    else
+    } else {
         run_any<8>(w, x, rows, y, a.y_bf16, y_stride, a.s);
+    }
     return (int)hipGetLastError();
 }
 

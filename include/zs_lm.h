@@ -57,10 +57,12 @@ typedef enum zs_dtype { ZS_DTYPE_BF16 = 0, ZS_DTYPE_F32 = 1 } zs_dtype;
  * them; nothing else of the payload is read. Any tensor offset, width, shard
  * length and block (a power of two in [8, 256]) is accepted; products run at
  * the memory's speed where tensor offset, in_features and shard length are
- * multiples of block and block >= 32, and slower elsewhere. A block whose
- * scale is NaN (an infinity or NaN among its parameters) gives NaN.
+ * multiples of block and block >= 32, slower where they are not, and slowest
+ * with smaller blocks. A block whose
+ * scale is NaN (an infinity or NaN among its parameters) gives NaN, and an
+ * infinity or NaN in x gives infinities or NaN in its row of y.
  *
- * FLAT plans. bits 4 or 8. out_features <= 2^25, in_features <= 2^30. x is bf16, y bf16 or fp32 (y_dtype).
+ * FLAT plans. bits 4 or 8. out_features <= 2^25, in_features <= 2^29. x is bf16, y bf16 or fp32 (y_dtype).
  * 0 <= rows <= ZS_QUANT_MATVEC_MAX_ROWS (more rows: dequantize once and use a
  * matrix product); rows == 0 or out_features == 0 does nothing, in_features
  * == 0 gives zeros. y may not overlap any input. */

@@ -73,6 +73,10 @@ LAYOUTS = [
     (9, 1, 2, 0, 0, 1),
     (3, 31, 5, 7, 0, 1),
     (257, 2048, 8, 2048, 8, 128),
+    (600, 777, 7, 40, 3, 8),        # shards that end inside rows, with last blocks of any length
+    (90, 1001, 16, 13, 0, 1),
+    (64, 640, 5, 8, 16, 8),
+    (33, 33, 3, 1, 2, 1),
 ]
 
 
