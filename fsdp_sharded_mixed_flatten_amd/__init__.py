@@ -773,6 +773,18 @@ def _lm_array(t, dtype, numel, cols, device, what):
     return t.data_ptr()
 
 
+def _lm_flat(t, dtypes, need, device, what):
+    """Address of a contiguous buffer of at least `need` elements (an integer is taken as the address itself)."""
+    if isinstance(t, int):
+        return t
+    if t.get_device() != device:
+        raise _lm_elsewhere(t, device, what)
+    if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"{what} must hold at least {need} contiguous elements of {dtypes[0]}, got {t.numel()} of "
+                         f"{t.dtype}")
+    return t.data_ptr()
+
+
 def _lm_call(fn, device, stream, *args):
     """Runs fn(*args, stream) with the call's device current."""
     torch = _torch
@@ -829,14 +841,10 @@ def zs_quant_matvec(plan, tensor, out_features, in_features, bits, block, codes_
     else:
         raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
     S, N = plan.shape
-    if not isinstance(codes_all, int) and codes_all.get_device() != device:
-        raise _lm_elsewhere(codes_all, device, "codes_all")
-    if not isinstance(scales_all, int) and scales_all.get_device() != device:
-        raise _lm_elsewhere(scales_all, device, "scales_all")
     _lm_call(_lib.zs_quant_matvec, device, stream, plan.handle, tensor, out_features, in_features, bits, block,
-             _ptr(codes_all, "bytes", N * S * bits // 8, "codes_all"),
-             _ptr(scales_all, "f32", N * -(-S // max(block, 1)), "scales_all"), x.data_ptr(), xs, rows, y.data_ptr(),
-             y_dtype, ys)
+             _lm_flat(codes_all, (_torch.uint8, _torch.int8), N * S * bits // 8, device, "codes_all"),
+             _lm_flat(scales_all, (_torch.float32,), N * -(-S // max(block, 1)), device, "scales_all"), x.data_ptr(),
+             xs, rows, y.data_ptr(), y_dtype, ys)
 
 
 def zs_token_logprobs(logits, tokens, temperature=1.0, logprob=None, entropy=None, stats=None, top_ids=None,

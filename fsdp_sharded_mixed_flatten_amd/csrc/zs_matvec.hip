@@ -42,7 +42,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // ------------------------------------------------------------------ any layout
-// Blocks of 8 and 16, rows of less than 32 columns and shards shorter than a row.
+// Blocks of 8, blocks of 16 out of line with the rows, rows of less than 32
+// columns and shards shorter than a row.
 // One wave per row of W and M rows of x. The wave walks the row in units of 8
 // elements of the flat buffer that start at multiples of 8: a unit never
 // crosses a shard (S is a multiple of 8) or a block (blocks start at multiples
@@ -335,6 +336,7 @@ struct Span {
 // of A left out: two partial sums, each with its own scale. Where a shard's
 // last block is shorter than 32, the window around it holds a third, C. Scales
 // follow one another from boundary to boundary, also from one shard to the next.
+// Whole blocks of 16 go this way too: A and B are then halves of a window.
 //
 // A row's first code may lie at any 4 or 8 bits: a lane loads the words around
 // its 32 codes and shifts them into place. Lane (g, r) works out boundary and
@@ -789,8 +791,10 @@ int launch_quant_matvec(const QuantWeight& w, Rows x, int rows, void* y, int y_d
     const int64_t block = int64_t(1) << w.block_shift;
     const bool four = w.bits == 4;
     const bool whole = w.off % block == 0 && w.n_in % block == 0 && w.shard % block == 0;
-    // split blocks: at most one shard's end in a row
-    const bool split = w.shard >= w.n_in;
+    // split blocks: at most one shard's end in a row, and no more than two
+    // boundaries inside 32 columns (whole blocks of 16 have one: 8192 x 8192 int4
+    // with 16 rows 41 us against 94 a wave a row, with one 31 against 23)
+    const bool split = w.shard >= w.n_in && (block >= 32 || (block == 16 && whole && rows > 4));
     if (block >= 32 && w.n_in > 0 && whole) {
         switch (w.block_shift) {
             case 5: four ? run_block<Whole4x32>(a) : run_block<Whole8x32>(a); break;
@@ -798,7 +802,7 @@ int launch_quant_matvec(const QuantWeight& w, Rows x, int rows, void* y, int y_d
             case 7: four ? run_block<Whole4x128>(a) : run_block<Whole8x128>(a); break;
             default: four ? run_block<Whole4x256>(a) : run_block<Whole8x256>(a); break;
         }
-    } else if (block >= 32 && w.n_in >= 32 && split) {
+    } else if (w.n_in >= 32 && split) {
         four ? run_block<Split4>(a) : run_block<Split8>(a);
     } else if (four) {
         run_any<4>(w, x, rows, y, a.y_bf16, y_stride, a.s);
