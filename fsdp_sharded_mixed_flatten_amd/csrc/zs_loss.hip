@@ -95,6 +95,63 @@ __device__ __forceinline__ void store_at(T* row, int64_t first, u32x4 v) {
         *p = v;
 }
 
+// ------------------------------------------------------------------ reductions over lanes
+// By data-parallel-primitive moves, an instruction a step (a shuffle through
+// shared memory is an instruction, an address and its latency).
+
+// v moved by CTRL; lanes that nothing moves into get `none`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float moved(float v, float none) {
+    return __uint_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_uint(none), __float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+constexpr int kShr = 0x110, kMirror = 0x140, kHalfMirror = 0x141, kBcast15 = 0x142, kBcast31 = 0x143;
+constexpr int kQuadSwap1 = 0xB1, kQuadSwap2 = 0x4E;  // lanes 1 0 3 2 and 2 3 0 1 of each four
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// Over the 64 lanes, the same in all: rows of 16 first, then across them.
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, moved<kShr + 1>(v, -kInf));
+    v = fmaxf(v, moved<kShr + 2>(v, -kInf));
+    v = fmaxf(v, moved<kShr + 4>(v, -kInf));
+    v = fmaxf(v, moved<kShr + 8>(v, -kInf));
+    v = fmaxf(v, moved<kBcast15, 0xA>(v, -kInf));
+    v = fmaxf(v, moved<kBcast31, 0xC>(v, -kInf));
+    return lane_value(v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v += moved<kShr + 1>(v, 0.0f);
+    v += moved<kShr + 2>(v, 0.0f);
+    v += moved<kShr + 4>(v, 0.0f);
+    v += moved<kShr + 8>(v, 0.0f);
+    v += moved<kBcast15, 0xA>(v, 0.0f);
+    v += moved<kBcast31, 0xC>(v, 0.0f);
+    return lane_value(v, 63);
+}
+
+// Over groups of W = 4, 8 or 16 lanes, the same in all of a group.
+template <int W>
+__device__ __forceinline__ float group_max(float v) {
+    v = fmaxf(v, moved<kQuadSwap1>(v, v));
+    v = fmaxf(v, moved<kQuadSwap2>(v, v));
+    if (W > 4) v = fmaxf(v, moved<kHalfMirror>(v, v));
+    if (W > 8) v = fmaxf(v, moved<kMirror>(v, v));
+    return v;
+}
+
+template <int W>
+__device__ __forceinline__ float group_sum(float v) {
+    v += moved<kQuadSwap1>(v, v);
+    v += moved<kQuadSwap2>(v, v);
+    if (W > 4) v += moved<kHalfMirror>(v, v);
+    if (W > 8) v += moved<kMirror>(v, v);
+    return v;
+}
+
 // Gradients are not read here again: nontemporal stores leave the caches to the
 // logits (4096 x 32000 bf16 87 us against 107, 1024 x 151936 fp32 321 against
 // 381). Not where rows start inside a 16-byte unit: a line then takes two
@@ -295,23 +352,20 @@ __device__ __forceinline__ Fast fast_running(Fast r, const T* row, int first, in
     return r;
 }
 
+// The block's sums, the same in every thread: the maximum first, then each lane
+// moves its sums to it once. THREADS / 64 entries of `part`.
 template <int THREADS, bool ENTROPY>
 __device__ __forceinline__ Fast fast_block_merge(Fast r, float k, Fast* part) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const Fast o{__shfl_xor(r.m, d, 64), __shfl_xor(r.c, d, 64), __shfl_xor(r.s, d, 64),
-                     ENTROPY ? __shfl_xor(r.t, d, 64) : 0.0f};
-        r = fast_merge<ENTROPY>(r, o, k);
-    }
+    constexpr int W = THREADS / 64;
+    fast_rebase<ENTROPY>(r, wave_max(r.m), k);
+    r.s = wave_sum(r.s);
+    if (ENTROPY) r.t = wave_sum(r.t);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = r;
     __syncthreads();
-    r = part[threadIdx.x & (THREADS / 64 - 1)];
-#pragma unroll
-    for (int d = THREADS / 128; d; d >>= 1) {
-        const Fast o{__shfl_xor(r.m, d, 64), __shfl_xor(r.c, d, 64), __shfl_xor(r.s, d, 64),
-                     ENTROPY ? __shfl_xor(r.t, d, 64) : 0.0f};
-        r = fast_merge<ENTROPY>(r, o, k);
-    }
+    r = part[threadIdx.x % W];
+    fast_rebase<ENTROPY>(r, group_max<W>(r.m), k);
+    r.s = group_sum<W>(r.s);
+    if (ENTROPY) r.t = group_sum<W>(r.t);
     return r;
 }
 
@@ -348,7 +402,20 @@ __device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float
 // ------------------------------------------------------------------ best alternatives
 
 // Whether logit a of token i comes before logit b of token j.
-__device__ __forceinline__ bool before(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
+__device__ __forceinline__ bool before(float a, int i, float b, int j) { return (a > b) | ((a == b) & (i < j)); }
+
+// The same order as one number, larger first: the logit's bits, made to grow
+// with it (-0 as +0), over the token's, made to shrink.
+__device__ __forceinline__ uint64_t order_key(float x, int id) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    const uint32_t up = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return ((uint64_t)up << 32) | (0xFFFFFFFFu - (uint32_t)id);
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+    const uint32_t up = (uint32_t)(key >> 32);
+    return __uint_as_float((up & 0x80000000u) ? up ^ 0x80000000u : ~up);
+}
+__device__ __forceinline__ int key_token(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // The thread's first element that comes after (x0, i0) in the order of
 // `before`; token INT32_MAX if there is none.
@@ -387,9 +454,8 @@ __device__ __forceinline__ void next_own(const T* row, int64_t vocab, float x0, 
 // own elements that has not been taken, the best of those is taken, and the
 // thread it came from looks for its next. Right for any row (equal or masked
 // logits included). Every logit is below +infinity and no NaN.
-template <typename T, int THREADS>
-__device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int top, float m, float inv_t,
-                                              float logsum, int32_t* ids, float* lps, float* lx, int* li) {
+template <typename T, int THREADS, typename Put>
+__device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int top, float* lx, int* li, Put put) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float b;
     int bi;
@@ -417,17 +483,15 @@ __device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int t
                 i = li[w];
             }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            ids[n] = i;
-            lps[n] = m == -kInf ? -kInf : (x - m) * inv_t - logsum;
-        }
+        if (threadIdx.x == 0) put(n, x, i);
         if (bi == i) next_own<T, THREADS>(row, vocab, x, i, &b, &bi);
     }
 }
 
-// The row's `top` best elements. 64 groups of threads cover the row; the
-// top-th largest of the groups' maxima is a bound that at least `top` elements
-// reach and, the elements being spread over the groups, few more do: the
+// The row's `top` best elements, put(place, logit, token) for each; own: this
+// thread's largest logit. 64 groups of threads cover the row; the
+// top-th largest of the groups' maxima, or a little less, is a bound that at
+// least `top` elements reach and, the elements being spread over the groups, few more do: the
 // elements of the threads whose own maximum reaches it are read again (they
 // come from a cache), those that reach it are listed, and the list is ranked by
 // counting. The second reading is dealt out over the whole block: left to the
@@ -437,46 +501,82 @@ __device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int t
 constexpr int kListed = 512;
 struct TopShared {
     float group[64];
-    float x[kListed];
-    int id[kListed];
+    uint64_t key[kListed];  // order_key of the listed elements
+    float best[16];         // of the waves, for top_by_rounds
+    int best_id[16];
     int owner[1024];
     int n, owners;
 };
 
-template <typename T, int THREADS>
-__device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int top, const RowStats& st, float inv_t,
-                                             int32_t* ids, float* lps, TopShared& sh) {
-    constexpr int N = Vec<T>::kN;
+//
+// The bound; sh.n and sh.owners are 0 afterwards.
+template <int THREADS>
+__device__ __forceinline__ float top_bound(int top, float own, TopShared& sh) {
     constexpr int kGroup = THREADS / 64;  // threads a group
     const int lane = threadIdx.x & 63;
-    float g = st.own;
-#pragma unroll
-    for (int d = 1; d < kGroup; d <<= 1) g = fmaxf(g, __shfl_xor(g, d, 64));
+    const float g = group_max<kGroup>(own);
     if (threadIdx.x % kGroup == 0) sh.group[threadIdx.x / kGroup] = g;
     if (threadIdx.x == 0) sh.n = sh.owners = 0;
     __syncthreads();
-    // the bound: the smallest group maximum that fewer than `top` others exceed
-    g = sh.group[lane];
-    int above = 0;
-#pragma unroll 16
-    for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i)) > g;
-    float bound = above < top ? g : kInf;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) bound = fminf(bound, __shfl_xor(bound, d, 64));
-    auto list = [&](float f, int at) {
-        if (f >= bound) {
-            const int n = atomicAdd(&sh.n, 1);
-            if (n < kListed) {
-                sh.x[n] = f;
-                sh.id[n] = at;
-            }
+    // the largest number of 16 leading bits that at least `top` groups' maxima
+    // reach, in the order of order_key
+    const uint32_t key = (uint32_t)(order_key(sh.group[lane], 0) >> 32);
+    uint32_t reach = 0;
+    for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
+        if ((int)__popcll(__ballot(key >= (reach | bit))) >= top) reach |= bit;
+    // nothing lies between -infinity and the first 16 bits' value below it
+    return reach <= 0x007F0000u ? -kInf : key_logit((uint64_t)reach << 32);
+}
+
+__device__ __forceinline__ void top_list(float f, int at, TopShared& sh) {
+    const int n = atomicAdd(&sh.n, 1);
+    if (n < kListed) sh.key[n] = order_key(f, at);
+}
+
+// Ranks the list.
+template <typename T, int THREADS, typename Put>
+__device__ __forceinline__ void top_rank(const T* row, int64_t vocab, int top, TopShared& sh, Put put) {
+    const int lane = threadIdx.x & 63;
+    __syncthreads();
+    const int n = sh.n;
+    if (n > kListed) {
+        __syncthreads();
+        top_by_rounds<T, THREADS>(row, vocab, top, sh.best, sh.best_id, put);
+        return;
+    }
+    if (n <= 64) {  // the usual list: one wave, an entry a lane
+        if (threadIdx.x >= 64) return;
+        const uint64_t key = sh.key[lane];
+        int place = 0;
+        for (int o = 0; o < n; ++o) {
+            const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), o) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)key, o);
+            place += other > key;
         }
-    };
+        if (lane < n && place < top) put(place, key_logit(key), key_token(key));
+        return;
+    }
+    for (int c = threadIdx.x; c < n; c += THREADS) {
+        const uint64_t key = sh.key[c];
+        int place = 0;
+#pragma unroll 8
+        for (int o = 0; o < n; ++o) place += sh.key[o] > key;
+        if (place < top) put(place, key_logit(key), key_token(key));
+    }
+}
+
+template <typename T, int THREADS, typename Put>
+__device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int top, float own, TopShared& sh, Put put) {
+    constexpr int N = Vec<T>::kN;
+    const float bound = top_bound<THREADS>(top, own, sh);
     const int64_t nv = vocab / N;
-    if (st.own >= bound) {
+    if (own >= bound) {
         sh.owner[atomicAdd(&sh.owners, 1)] = threadIdx.x;
         const int64_t tail = nv * N + threadIdx.x;
-        if (tail < vocab) list(Vec<T>::one(row[tail]), (int)tail);
+        if (tail < vocab) {
+            const float f = Vec<T>::one(row[tail]);
+            if (f >= bound) top_list(f, (int)tail, sh);
+        }
     }
     __syncthreads();
     // the listed threads' vectors, dealt out over the block: vector j of thread
@@ -501,45 +601,51 @@ __device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int to
             for (int i = 0; i < N; ++i) reach |= Vec<T>::get(x[u], i) >= bound ? 1u << i : 0u;
             for (; reach; reach &= reach - 1) {
                 const int at = (int)v[u] * N + __ffs(reach) - 1;
-                list(Vec<T>::one(row[at]), at);
+                top_list(Vec<T>::one(row[at]), at, sh);
             }
         }
     }
-    __syncthreads();
-    const int n = sh.n;
-    if (n > kListed) {
-        __syncthreads();
-        top_by_rounds<T, THREADS>(row, vocab, top, st.m, inv_t, st.logsum, ids, lps, sh.x, sh.id);
-        return;
-    }
-    auto put = [&](int place, float x, int id) {
-        if (place < top) {
-            ids[place] = id;
-            lps[place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
-        }
-    };
-    if (n <= 64) {  // the usual list: one wave, an entry a lane
-        if (threadIdx.x >= 64) return;
-        const float x = sh.x[lane];
-        const int id = sh.id[lane];
-        int place = 0;
-        for (int o = 0; o < n; ++o) {
-            const float ox = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), o));
-            place += before(ox, (int)__builtin_amdgcn_readlane(id, o), x, id);
-        }
-        if (lane < n) put(place, x, id);
-        return;
-    }
-    for (int c = threadIdx.x; c < n; c += THREADS) {
-        const float x = sh.x[c];
-        const int id = sh.id[c];
-        int place = 0;
-        for (int o = 0; o < n; ++o) place += before(sh.x[o], sh.id[o], x, id);
-        put(place, x, id);
-    }
+    top_rank<T, THREADS>(row, vocab, top, sh, put);
 }
 
 // ------------------------------------------------------------------ log-probabilities
+
+// The outputs of a row that is skipped.
+__device__ __forceinline__ void skipped_row(int64_t r, const LogprobsOut& out) {
+    if (threadIdx.x == 0) {
+        if (out.logprob) out.logprob[r] = 0.0f;
+        if (out.entropy) out.entropy[r] = 0.0f;
+        if (out.stats) out.stats[2 * r] = out.stats[2 * r + 1] = 0.0f;
+    }
+    if ((int)threadIdx.x < out.top) {
+        out.top_ids[r * out.top + threadIdx.x] = -1;
+        out.top_logprobs[r * out.top + threadIdx.x] = 0.0f;
+    }
+}
+
+// The given token's logit, NaN where it is past the vocabulary.
+template <typename T>
+__device__ __forceinline__ float token_logit(const T* row, int64_t token, int64_t vocab) {
+    return token < vocab ? Vec<T>::one(row[token]) : quiet_nan();
+}
+
+// A row's outputs but for its alternatives; those too where it has none (a NaN
+// or +infinity in the row: log s is NaN). x: the given token's logit.
+__device__ __forceinline__ void row_outputs(int64_t r, const RowStats& st, float x, float inv_t,
+                                            const LogprobsOut& out) {
+    if (threadIdx.x == 0) {
+        if (out.logprob) out.logprob[r] = st.m == -kInf && x == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+        if (out.entropy) out.entropy[r] = st.logsum - kLn2 * st.mean_d;
+        if (out.stats) {
+            out.stats[2 * r] = st.m;
+            out.stats[2 * r + 1] = st.logsum;
+        }
+    }
+    if (!(st.logsum < kInf) && (int)threadIdx.x < out.top) {
+        out.top_ids[r * out.top + threadIdx.x] = -1;
+        out.top_logprobs[r * out.top + threadIdx.x] = quiet_nan();
+    }
+}
 
 template <typename T, int THREADS, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logits, int64_t stride, int64_t vocab,
@@ -550,44 +656,18 @@ __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logi
     const int64_t r = blockIdx.x;
     const T* row = logits + r * stride;
     const int64_t token = tokens[r];
-    int32_t* ids = out.top_ids + r * out.top;
-    float* lps = out.top_logprobs + r * out.top;
     if (token < 0) {
-        if (threadIdx.x == 0) {
-            if (out.logprob) out.logprob[r] = 0.0f;
-            if (out.entropy) out.entropy[r] = 0.0f;
-            if (out.stats) out.stats[2 * r] = out.stats[2 * r + 1] = 0.0f;
-        }
-        if ((int)threadIdx.x < out.top) {
-            ids[threadIdx.x] = -1;
-            lps[threadIdx.x] = 0.0f;
-        }
+        skipped_row(r, out);
         return;
     }
+    const float x = token_logit(row, token, vocab);
     const RowStats st = row_stats<T, THREADS, ENTROPY>(row, vocab, k, part);
-    const bool empty = st.m == -kInf;
-    const bool bad = !(st.logsum < kInf);  // a NaN or +infinity in the row
-    if (threadIdx.x == 0) {
-        if (out.logprob) {
-            float lp = quiet_nan();
-            if (token < vocab) lp = empty ? -kInf : (Vec<T>::one(row[token]) - st.m) * inv_t - st.logsum;
-            out.logprob[r] = lp;
-        }
-        if (out.entropy) out.entropy[r] = st.logsum - kLn2 * st.mean_d;
-        if (out.stats) {
-            out.stats[2 * r] = st.m;
-            out.stats[2 * r + 1] = st.logsum;
-        }
-    }
-    if (out.top == 0) return;
-    if (bad) {
-        if ((int)threadIdx.x < out.top) {
-            ids[threadIdx.x] = -1;
-            lps[threadIdx.x] = quiet_nan();
-        }
-        return;
-    }
-    top_elements<T, THREADS>(row, vocab, out.top, st, inv_t, ids, lps, sh);
+    row_outputs(r, st, x, inv_t, out);
+    if (out.top == 0 || !(st.logsum < kInf)) return;
+    top_elements<T, THREADS>(row, vocab, out.top, st.own, sh, [&](int place, float x, int id) {
+        out.top_ids[r * out.top + place] = id;
+        out.top_logprobs[r * out.top + place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+    });
 }
 
 // ------------------------------------------------------------------ gradient of the log-probabilities
@@ -646,18 +726,6 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
 }
 
 // ------------------------------------------------------------------ distillation
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
-}
 
 template <typename T>
 __device__ __forceinline__ void fill_row(T* g, int64_t vocab, float f) {

@@ -82,7 +82,7 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
  *   top_logprobs[r, i] = its log-probability
  * A logit of -infinity is a masked token: probability 0, log-probability
  * -infinity, nothing added to the entropy.
- *   tokens[r] < 0       the row is skipped: its logits are not read, every
+ *   tokens[r] < 0       the row is skipped: its logits do not matter, every
  *                       fp32 output of it is 0 and its top_ids are -1.
  *   tokens[r] >= vocab  logprob[r] is NaN, the other outputs as usual.
  *   every logit -infinity   logprob -infinity, entropy 0, stats { -infinity,
@@ -124,7 +124,7 @@ zs_status zs_token_logprobs_backward(const void* logits, int32_t dtype, int64_t 
  * token masked in the student (-infinity) that has q > 0 makes the loss
  * infinite, its gradient staying finite.
  *   row_weight[r] == 0, or no used entry with q > 0   loss 0, gradient 0; the
- *                       row's logits are not read.
+ *                       row's logits do not matter.
  *   every student logit -infinity   p = 0.
  *   an id >= vocab, a NaN or +infinity among the row's logits or used teacher
  *   logits              loss and the row's whole gradient are NaN.

@@ -155,7 +155,7 @@ def _special_rows(vocab):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("vocab", [40, 3000, 40001])
+@pytest.mark.parametrize("vocab", [40, 3000, 40001, 110003])
 def test_logprobs_masks_ties_and_specials(zs, vocab, dtype):
     import torch
     rows = _special_rows(vocab)
