@@ -588,18 +588,22 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
     if (g < rows && o < w.n_out) store_y(y, y_bf16, g * y_stride + o, v * Codes<S::kBits>::kUnit);
 }
 
-// 5 and more rows of x, in MT tiles of 16: what costs here is bringing x to the
-// waves (each needs all of it), so RW waves with 16 rows of W each share a
-// span of x in shared memory, and KW such groups take turns over the spans.
+// 5 and more rows of x, MT tiles of 16 a workgroup (further tiles take further
+// workgroups, which find the codes in a cache): what costs here is bringing x
+// to the waves (each needs all of it), so RW waves with 16 rows of W each share
+// a span of x in shared memory, and KW such groups take turns over the spans.
 // One barrier a turn; x of the next turn is loaded beside its codes and goes
 // into the other half of the buffer.
-// 28672 x 8192 int4 with 16 rows: 44 us against 76 with each wave loading its
-// own operands, 64 rows 118 against 258; at 2048 x 11008 with 16 rows 9.2
+// 28672 x 8192 int4 with 16 rows: 43 us against 76 with each wave loading its
+// own operands, 64 rows 97 against 258; at 2048 x 11008 with 16 rows 9.2
 // against 10.8.
 template <typename S, int MT, int RW, int KW>
 __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, const uint16_t* __restrict__ x,
                                                               int64_t x_stride, int rows, void* __restrict__ y,
                                                               int y_bf16, int64_t y_stride) {
+    const int row0 = blockIdx.y * (16 * MT);  // this workgroup's first row of x
+    x += row0 * x_stride;
+    rows = rows - row0 < 16 * MT ? rows - row0 : 16 * MT;
     constexpr int SPAN = S::SPAN;
     constexpr int kSpan = SPAN * kChunk;
     constexpr int kUnits = kSpan / 8;           // 16-byte units of a row of x in a span
@@ -697,7 +701,7 @@ __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 16 * m + 4 * i + g;
-            if (row < rows) store_y(y, y_bf16, row * y_stride + o, acc[m][i] * Codes<S::kBits>::kUnit);
+            if (row < rows) store_y(y, y_bf16, (row0 + row) * y_stride + o, acc[m][i] * Codes<S::kBits>::kUnit);
         }
 }
 
@@ -727,37 +731,69 @@ void run_few(const Product& a) {
 
 template <typename S, int MT, int RW, int KW>
 void run_rows(const Product& a) {
-    hipLaunchKernelGGL((k_matvec_rows<S, MT, RW, KW>), dim3((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW))),
-                       dim3(64 * RW * KW), 0, a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y,
+    const dim3 grid((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW)), (unsigned)((a.rows + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((k_matvec_rows<S, MT, RW, KW>), grid, dim3(64 * RW * KW), 0, a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y,
                        a.y_bf16, a.y_stride);
 }
 
-// S<SPAN>: what loads W, in spans of SPAN chunks.
+// S<SPAN>: what loads W, in spans of SPAN chunks. The choices were measured
+// against each other (1 to 4 tiles of x, 1 to 8 waves that share it, 1 to 16
+// groups that split the columns, spans of 1 to 4) at the sizes in the comments
+// (columns x rows of W), int4, in us.
 template <template <int> class S>
 void run_block(const Product& a) {
-    // Where 128 rows of W a workgroup still fill the chip, all 8 waves share x
-    // (8192 x 128256 int4, 16 rows: 131 us against 192 with 4 groups of 4);
-    // elsewhere 2 do and 4 groups split the columns (28672 x 8192: 44 us
-    // against 68 with 2 groups of 4).
-    const bool wide = a.w.n_out >= 128 * 256;
+    constexpr bool kSplit = S<1>::kRagged;
+    const int64_t n_out = a.w.n_out;
+    // From here on 128 rows of W a workgroup fill the chip and all 8 waves share
+    // x (8192 x 128256, 16 rows: 131 against 192 with 4 groups of 4).
+    const bool wide = n_out >= 128 * 256;
+    // Up to here 32 rows a workgroup leave compute units idle: fewer rows of W
+    // and of x each, the tiles of x in workgroups of their own.
+    const bool narrow = n_out <= 4096;
     if (a.rows == 1)
         run_few<S<4>, 1>(a);
     else if (a.rows <= 4)
         run_few<S<4>, 4>(a);
-    else if (a.rows <= 16 && wide)
-        run_rows<S<4>, 1, 8, 1>(a);
-    else if (a.rows <= 16 && a.w.n_in > 2048)
-        run_rows<S<4>, 1, 2, 4>(a);
-    else if (a.rows <= 16)  // shorter spans where the long ones make one turn (2048 x 11008: 9.2 us against 11.6)
-        run_rows<S<2>, 1, 2, 4>(a);
-    else if (a.rows <= 32 && wide)
-        run_rows<S<2>, 2, 8, 1>(a);
-    else if (a.rows <= 32)
-        run_rows<S<2>, 2, 2, 4>(a);
-    else if (wide)
+    else if (a.rows <= 16) {
+        if (wide)
+            run_rows<S<4>, 1, 8, 1>(a);
+        else if constexpr (kSplit) {
+            if (n_out <= 8192)  // 8191 x 8191: 31 against 39
+                run_rows<S<1>, 1, 1, 8>(a);
+            else
+                run_rows<S<2>, 1, 2, 4>(a);
+        } else if (narrow)  // 4096 x 4096: 7.5 against 8.4, 8192 x 512: 10.4 against 12.2
+            run_rows<S<2>, 1, 1, 8>(a);
+        else if (n_out <= 8192 && a.w.n_in > 2048)  // 28672 x 8192: 43 against 57
+            run_rows<S<4>, 1, 2, 4>(a);
+        else  // 4096 x 16384: 12.2 against 15.9, 2048 x 11008: 9.2 against 11.6
+            run_rows<S<2>, 1, 2, 4>(a);
+    } else if (a.rows <= 32) {
+        if (wide)
+            run_rows<S<2>, 2, 8, 1>(a);
+        else if constexpr (kSplit) {
+            if (narrow)  // 7253 x 271: 24 against 46
+                run_rows<S<1>, 1, 1, 8>(a);
+            else
+                run_rows<S<2>, 2, 2, 4>(a);
+        } else if (narrow)  // 4096 x 4096: 10.4 against 12.2
+            run_rows<S<2>, 1, 2, 4>(a);
+        else  // 8192 x 8192: 22.7 against 25.9
+            run_rows<S<2>, 2, 2, 4>(a);
+    } else if (wide) {
         run_rows<S<1>, 4, 8, 1>(a);
-    else
+    } else if constexpr (kSplit) {
+        if (narrow)  // 1995 x 3769, 60 rows: 15.5 against 21.8
+            run_rows<S<1>, 2, 2, 4>(a);
+        else  // 8191 x 8191, 40 rows: 62 against 88
+            run_rows<S<1>, 4, 2, 4>(a);
+    } else if (narrow) {  // 4096 x 4096, 64 rows: 12.3 against 19.0
+        run_rows<S<2>, 2, 2, 4>(a);
+    } else if (S<1>::kBits == 4) {  // 28672 x 8192, 64 rows: 97 against 121
+        run_rows<S<1>, 2, 2, 4>(a);
+    } else {  // 8 bits, read twice by two tiles of x: 2304 x 13200, 53 rows 24 against 31
         run_rows<S<1>, 4, 2, 4>(a);
+    }
 }
 
 template <int SPAN>
