@@ -181,12 +181,15 @@ def test_optional_outputs(zs):
 # ---------------------------------------------------------------- gradient of the log-probabilities
 
 
-def _grad_tol(ref, mag, vocab, dtype, z, temperature):
-    """mag: the terms' magnitude before they cancel."""
+def _grad_tol(ref, mag, vocab, dtype, z, temperature, factor):
+    """mag: the terms' magnitude before they cancel. factor: what a probability is multiplied with at most, a number a
+    row: an exponential below 2^-126 counts as 0, which takes up to 2^-126 from a probability (exponentials are
+    divided by a sum that is at least about 1) and so up to 2^-126 factor from the gradient."""
     with np.errstate(invalid="ignore"):
         spread = np.nanmax(np.where(np.isfinite(z), z, -INF), axis=1, keepdims=True) - z
         l = np.where(np.isfinite(spread), np.minimum(spread / temperature, 110.0), 0) + math.log(vocab + 1)
-    return mag * (2 * tol_s(vocab) + 16 * U + 8 * U * l) + _half_step(dtype) * np.abs(ref) * (1 + 1e-3) + 2.0 ** -126
+    return mag * (2 * tol_s(vocab) + 16 * U + 8 * U * l) + _half_step(dtype) * np.abs(ref) * (1 + 1e-3) \
+        + 2.0 ** -126 * (1 + np.asarray(factor)[:, None])
 
 
 def _check_gradient(zs, z, tokens, temperature, with_entropy, grad=None):
@@ -207,7 +210,11 @@ def _check_gradient(zs, z, tokens, temperature, with_entropy, grad=None):
     if with_entropy:
         mag = mag + np.abs(gh.cpu().numpy())[:, None] * 2 * (2 + math.log(vocab + 1)) / temperature * np.exp(
             np.array([lm.row_softmax(r, temperature)[2] for r in host]))
-    _near(g.double().cpu().numpy(), ref, _grad_tol(ref, mag, vocab, dtype, host, temperature), "grad_logits")
+    # |l| where p is not 0 yet: below log 2^150
+    factor = np.abs(gl.cpu().numpy()) / temperature
+    if with_entropy:
+        factor = factor + np.abs(gh.cpu().numpy()) * (104 + math.log(vocab + 1)) / temperature
+    _near(g.double().cpu().numpy(), ref, _grad_tol(ref, mag, vocab, dtype, host, temperature, factor), "grad_logits")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -290,7 +297,7 @@ def _check_distill(zs, z, ids, teacher, temperature=1.0, weight=None, grad=None)
     g = torch.full((rows, vocab), 7.0, dtype=z.dtype, device="cuda") if grad is None else grad
     zs.zs_distill_topk(z, d_ids, d_teacher, loss, grad_logits=g, temperature=temperature, row_weight=d_w)
     assert torch.equal(alone.view(torch.int32), loss.view(torch.int32))
-    g_tol = _grad_tol(g_ref, g_mag, vocab, dtype, host, temperature) + g_mag * tol_q[:, None]
+    g_tol = _grad_tol(g_ref, g_mag, vocab, dtype, host, temperature, scale * temperature) + g_mag * tol_q[:, None]
     _near(g.double().cpu().numpy(), g_ref, g_tol, "grad_logits")
 
 
