@@ -281,36 +281,42 @@ __device__ __forceinline__ Fast fast_one(float x, float k) {
 template <typename T, bool ENTROPY, int U>
 __device__ __forceinline__ void fast_add(Fast& r, const u32x4 (&x)[U], float k) {
     constexpr int N = Vec<T>::kN;
-    float m = r.m, low = kInf;
+    float m = r.m;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float a = Vec<T>::get(x[u], i), b = Vec<T>::get(x[u], i + 1);
-            m = fmaxf(fmaxf(m, a), b);
-            if (ENTROPY) low = fminf(fminf(low, a), b);
-        }
+        for (int i = 0; i < N; i += 2) m = fmaxf(fmaxf(m, Vec<T>::get(x[u], i)), Vec<T>::get(x[u], i + 1));
     fast_rebase<ENTROPY>(r, m, k);
-    const bool masked = ENTROPY && __any(low == -kInf);  // d = -infinity, which t has to leave out
+    float t = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float s[N], t = 0.0f;
+        float s[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float d = __builtin_fmaf(Vec<T>::get(x[u], i), k, -r.c);
+            const float d = __builtin_fmaf(Vec<T>::get(x[u], i), k, -r.c);
             s[i] = exp2_raw(d);
-            if (ENTROPY) {
-                if (masked) d = fmaxf(d, kLowest);
-                t = __builtin_fmaf(s[i], d, t);
-            }
+            if (ENTROPY) t = __builtin_fmaf(s[i], d, t);
         }
 #pragma unroll
         for (int h = N / 2; h; h >>= 1)
 #pragma unroll
             for (int i = 0; i < h; ++i) s[i] += s[i + h];
         r.s += s[0];
-        r.t += t;
     }
+    if (ENTROPY && __any(t != t)) {  // a masked logit (0 times an infinite d), which t has to leave out, or a NaN
+        t = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            u32x4 z = x[u];
+            asm("" : "+v"(z));  // worked out again: nothing is kept for this
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float d = __builtin_fmaf(Vec<T>::get(z, i), k, -r.c);
+                t = __builtin_fmaf(exp2_raw(d), fmaxf(d, kLowest), t);
+            }
+        }
+    }
+    r.t += t;
 }
 
 // r and the row's vectors from `first` on, then its tail.
@@ -321,22 +327,23 @@ __device__ __forceinline__ Fast fast_running(Fast r, const T* row, int first, in
     const uint32_t none = Vec<T>::kNegInf;
     int v = first;  // of the block's first thread
     u32x4 x[U];
+    auto load = [&](u32x4(&to)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) to[u] = load_at(row, v + u * THREADS);
+        v += U * THREADS;
+    };
     if (v + U * THREADS <= nv) {  // whole groups, the next one's loads ahead of each group's arithmetic
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = load_at(row, v + u * THREADS);
+        u32x4 y[U];
+        load(x);
         while (true) {
-            const int w = v + U * THREADS;
-            const bool more = w + U * THREADS <= nv;
-            u32x4 y[U];
-            if (more) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) y[u] = load_at(row, w + u * THREADS);
-            }
+            const bool more = v + U * THREADS <= nv;
+            if (more) load(y);
             fast_add<T, ENTROPY>(r, x, k);
-            v = w;
             if (!more) break;
-#pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = y[u];
+            const bool again = v + U * THREADS <= nv;
+            if (again) load(x);
+            fast_add<T, ENTROPY>(r, y, k);
+            if (!again) break;
         }
     }
     if (v < nv) {
