@@ -641,7 +641,9 @@ __device__ __forceinline__ float token_logit(const T* row, int64_t token, int64_
 __device__ __forceinline__ void row_outputs(int64_t r, const RowStats& st, float x, float inv_t,
                                             const LogprobsOut& out) {
     if (threadIdx.x == 0) {
-        if (out.logprob) out.logprob[r] = st.m == -kInf && x == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+        // m is -infinity in a row of nothing else and in one with a NaN beside (log s is NaN)
+        const bool masked = st.m == -kInf && st.logsum == 0.0f && x == -kInf;
+        if (out.logprob) out.logprob[r] = masked ? -kInf : (x - st.m) * inv_t - st.logsum;
         if (out.entropy) out.entropy[r] = st.logsum - kLn2 * st.mean_d;
         if (out.stats) {
             out.stats[2 * r] = st.m;
@@ -699,7 +701,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(const T* logits,
     T* g = grad + r * grad_stride;
     const int token = in.tokens[r];
     const float m = in.stats[2 * r], logsum = in.stats[2 * r + 1];
-    const bool zero = token < 0 || m == -kInf;
+    const bool zero = token < 0 || (m == -kInf && logsum == 0.0f);
     const float gl = token >= vocab ? quiet_nan() : in.grad_logprob[r];
     const float gh = ENTROPY ? in.grad_entropy[r] : 0.0f;
     const float h = ENTROPY ? in.entropy[r] : 0.0f;

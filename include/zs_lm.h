@@ -103,8 +103,8 @@ zs_status zs_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int
  *                         - grad_entropy[r] * p_j * (l_j + entropy[r]) ) / temperature
  * of the logits' dtype. grad_entropy is optional; entropy (the forward call's)
  * is given with it. Skipped rows (token < 0) and rows whose every logit is
- * -infinity get zeros, rows whose token is >= vocab or whose log s is NaN get
- * NaN. grad_logits may be logits itself (same address and stride); otherwise
+ * -infinity get zeros, other rows whose token is >= vocab or whose log s is NaN
+ * get NaN. grad_logits may be logits itself (same address and stride); otherwise
  * the two may not overlap. */
 zs_status zs_token_logprobs_backward(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                      int64_t row_stride, const int32_t* tokens, float temperature,

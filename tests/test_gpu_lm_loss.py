@@ -237,6 +237,19 @@ def test_logprobs_gradient_specials(zs, dtype):
         _check_gradient(zs, z, [r[2] for r in rows], 1.0, with_entropy)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 9, 3001, 40001])
+def test_nan_among_masked_logits(zs, vocab, dtype):
+    """A NaN is not hidden by the row's maximum being -infinity."""
+    import torch
+    z = torch.full((3, vocab), -INF, dtype=_dtype(dtype), device="cuda")
+    z[0, 0] = z[1, vocab - 1] = z[2, vocab // 2] = NAN
+    tokens = [vocab - 1, 0, vocab // 3]
+    _check_forward(zs, z, tokens, 1.0, min(vocab, 4))
+    for with_entropy in (False, True):
+        _check_gradient(zs, z, tokens, 1.0, with_entropy)
+
+
 def test_gradient_equals_differences(zs):
     """The gradient against central differences of the forward call itself (fp32 logits, a step of 2^-5: truncation
     h^2 / 6 times a third derivative below 2 g, rounding 2 tol / 2h)."""
