@@ -16,8 +16,9 @@ constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;
 // counted in int32.
 constexpr int64_t kMaxOut = int64_t(1) << 25;
 constexpr int64_t kMaxIn = int64_t(1) << 29;
-// Largest row stride and matrix extent: byte addresses stay far inside int64.
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+// Largest row stride: 2^22 rows of 4-byte elements that far apart span 2^62
+// bytes, inside int64.
+constexpr int64_t kMaxStride = int64_t(1) << 38;
 
 int64_t elem_bytes(int32_t dtype) { return dtype == ZS_DTYPE_BF16 ? 2 : 4; }
 
@@ -40,7 +41,7 @@ zs_status check_opt_array(const void* p, uintptr_t align, const char* what) {
 
 zs_status check_stride(int64_t stride, int64_t cols, const char* what) {
     if (stride < cols || stride > kMaxStride)
-        return report(ZS_EINVAL, "%s = %lld outside [%lld, 2^40]", what, (long long)stride, (long long)cols);
+        return report(ZS_EINVAL, "%s = %lld outside [%lld, 2^38]", what, (long long)stride, (long long)cols);
     return ZS_OK;
 }
 
@@ -131,7 +132,8 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
         if (zs_status st = check_apart(ys, span(codes_all, plan->T * bits / 8), "y", "codes_all")) return st;
         if (zs_status st = check_apart(ys, span(scales_all, 4 * n_scales * plan->world), "y", "scales_all")) return st;
     }
-    zs::QuantWeight w{codes_all,  scales_all, t.flat_off, out_features, in_features, plan->S, n_scales, plan->world, bits, 0};
+    zs::QuantWeight w{codes_all, scales_all, t.flat_off,  out_features, in_features,
+                      plan->S,   n_scales,   plan->world, bits,         0};
     while ((1 << w.block_shift) < block) ++w.block_shift;
     zs::trace_call("zs_quant_matvec", plan, 0, t.flat_off, t.numel, stream);
     return zs::report_hip(zs::launch_quant_matvec(w, zs::Rows{x_bf16, x_stride}, rows, y, y_dtype, y_stride, stream),

@@ -78,6 +78,16 @@ def _logits_refusals(zs, fn, good):
     assert _call(fn, good, rows=0) == zs.ZS_OK
 
 
+def test_strides_whose_extent_leaves_64_bits(zs):
+    """(2^22 - 2) rows of fp32 2^40 elements apart end past 2^63 bytes."""
+    _expect(zs, zs.lib().zs_token_logprobs,
+            dict(LOGITS, dtype=1, tokens=_at(1), temperature=1.0, logprob=_at(2), entropy=None, stats=None, top=0,
+                 ids=None, lps=None, stream=None), zs.ZS_EINVAL, rows=(1 << 22) - 1, stride=1 << 40)
+    _expect(zs, zs.lib().zs_token_logprobs_backward,
+            dict(LOGITS, dtype=1, tokens=_at(1), temperature=1.0, stats=_at(2), entropy=None, grad_logprob=_at(4),
+                 grad_entropy=None, grad=_at(6), grad_stride=(1 << 38) + 1, stream=None), zs.ZS_EINVAL)
+
+
 def test_token_logprobs_refusals(zs):
     good = dict(LOGITS, tokens=_at(1), temperature=1.0, logprob=_at(2), entropy=_at(3), stats=_at(4), top=2,
                 ids=_at(5), lps=_at(6), stream=None)
