@@ -515,7 +515,6 @@ struct TopShared {
     int n, owners;
 };
 
-//
 // The bound; sh.n and sh.owners are 0 afterwards.
 template <int THREADS>
 __device__ __forceinline__ float top_bound(int top, float own, TopShared& sh) {
@@ -1068,18 +1067,25 @@ int run_grad(Rows logits, int64_t rows, int64_t vocab, double temperature, const
     // the row's vectors, and one thread for each element of its tail
     const int64_t per = kGradThreads * kGradU;
     const int64_t tiles = (vocab / N + vocab % N + per - 1) / per;
-    if (rows * tiles > ((int64_t(1) << 32) - 1) / kGradThreads) return (int)hipErrorInvalidValue;
-    const T* p = static_cast<const T*>(logits.p);
-    T* g = static_cast<T*>(grad);
+    // a launch covers at most 2^32 - 1 work-items: 4 million rows of 16392 bf16
+    // logits (137 GB, in place) take two
+    const int64_t most = ((int64_t(1) << 32) - 1) / kGradThreads / tiles;
     const float inv_t = (float)(1.0 / temperature), k = (float)(M_LOG2E / temperature);
-    const dim3 grid((unsigned)(rows * tiles));
-    if (in.grad_entropy)
-        hipLaunchKernelGGL((k_logprobs_grad<T, true>), grid, dim3(kGradThreads), 0, s, p, logits.stride, vocab,
-                           (unsigned)tiles, inv_t, k, in, g, grad_stride);
-    else
-        hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, s, p, logits.stride, vocab,
-                           (unsigned)tiles, inv_t, k, in, g, grad_stride);
-    return (int)hipGetLastError();
+    for (int64_t r = 0; r < rows; r += most) {
+        const T* p = static_cast<const T*>(logits.p) + r * logits.stride;
+        T* g = static_cast<T*>(grad) + r * grad_stride;
+        const LogprobsGradIn part{in.tokens + r, in.stats + 2 * r, in.entropy ? in.entropy + r : nullptr,
+                                  in.grad_logprob + r, in.grad_entropy ? in.grad_entropy + r : nullptr};
+        const dim3 grid((unsigned)((rows - r < most ? rows - r : most) * tiles));
+        if (in.grad_entropy)
+            hipLaunchKernelGGL((k_logprobs_grad<T, true>), grid, dim3(kGradThreads), 0, s, p, logits.stride, vocab,
+                               (unsigned)tiles, inv_t, k, part, g, grad_stride);
+        else
+            hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, s, p, logits.stride, vocab,
+                               (unsigned)tiles, inv_t, k, part, g, grad_stride);
+        if (const hipError_t e = hipGetLastError()) return (int)e;
+    }
+    return (int)hipSuccess;
 }
 
 }  // namespace

@@ -472,6 +472,35 @@ def test_rows_past_32_bit_offsets(zs):
     assert torch.equal(z[-2:], g_small) and not z[:-2].any()
 
 
+def test_gradient_of_more_work_than_a_launch(zs):
+    """2^22 - 1 rows of 5 workgroups each, in place: more work-items than 2^32. All but a few rows are skipped."""
+    import torch
+    rows, vocab = (1 << 22) - 1, 16392
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 138 GB of device memory")
+    z = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    split = ((1 << 32) - 1) // 256 // 5  # rows of the first launch
+    live = torch.tensor([0, split - 1, split, rows - 1], device="cuda")
+    part = _logits(4, vocab, "bf16", seed=4).cuda()
+    z[live] = part
+    z[split + 1] = 5.0  # a skipped row that has to become 0
+    tokens = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    tokens[live] = torch.tensor([0, 5, 16391, 77], dtype=torch.int32, device="cuda")
+    f, _ = _check_forward(zs, part, [0, 5, 16391, 77])
+    stats = torch.zeros(rows, 2, device="cuda")
+    stats[live] = f.out["stats"]
+    gl = torch.linspace(0.5, 1.5, rows, device="cuda")
+    want = torch.empty_like(part)
+    zs.zs_token_logprobs_backward(part, tokens[live], f.out["stats"], gl[live], want)
+    zs.zs_token_logprobs_backward(z, tokens, stats, gl, z)
+    assert torch.equal(z[live], want)
+    for r in (1, split - 2, split + 1, rows - 2):
+        assert not z[r].any()
+    del z
+    torch.cuda.empty_cache()
+
+
 def test_streams_and_graph(zs):
     """A forward call and its gradient captured together, replayed on new inputs with eager work between, on a side
     stream, and two at once."""
