@@ -1043,10 +1043,13 @@ void run_logprobs(Rows logits, int64_t rows, int64_t vocab, const int32_t* token
 int launch_logprobs(Rows logits, int dtype, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
                     const LogprobsOut& out, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    // 512 threads a row where rows are few or long, else 256 (bf16, 8
-    // alternatives: 4096 x 128256 197 us against 227, 512 x 128256 31 against
-    // 33; 4096 x 65536 114 against 127 the other way round)
-    const bool wide = vocab > 8192 && (rows <= 1024 || vocab >= 98304);
+    // 512 threads a row where rows are few or 128 KB and longer, else 256 (8
+    // alternatives; 512 threads against 256, us: 64 x 151936 fp32 16.5, 23.2;
+    // 4096 x 128256 bf16 189, 199; 4096 x 65536 bf16 102, 105; 4096 x 32000 fp32
+    // 95, 102; the other way round 4096 x 32000 bf16 70, 55; 4096 x 8192 bf16 50,
+    // 21; about even at 512 rows of 128256 and 32000)
+    const int64_t row_bytes = vocab * (dtype == ZS_DTYPE_BF16 ? 2 : 4);
+    const bool wide = vocab > 8192 && (rows <= 1024 || row_bytes >= 128000);
     if (dtype == ZS_DTYPE_BF16 && wide)
         run_logprobs<uint16_t, 512>(logits, rows, vocab, tokens, temperature, out, s);
     else if (dtype == ZS_DTYPE_BF16)

@@ -491,9 +491,10 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t* x, int k, int n_in) {
 // chunk that mostly repeat each other, and took 36 instead of 24.5 us at 28672
 // x 8192 int4). The waves of a workgroup share its 16 rows of W and take turns
 // over the spans; their sums meet in shared memory at the end.
-// Reads at 5.1 TB/s at 28672 x 8192 int4 (24.5 us, one row), 6.0 TB/s at 8192 x
-// 128256 int8 (180 us, 4 rows); bound by memory there and by latency in
-// products of a few MB (4096 x 4096 int4 4.6 us, an empty launch 1.6 us).
+// Reads at 4.7 TB/s at 28672 x 8192 int4 (26.6 us, one row), 5.2 TB/s at 8192 x
+// 128256 int8 (210 us, 4 rows, blocks of 128, fp32 results); bound by memory
+// there and by latency in products of a few MB (4096 x 4096 int4 4.6 us, an
+// empty launch 1.6 us).
 template <typename S, int ROWS>
 __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_t* __restrict__ x, int64_t x_stride,
                                                     int rows, void* __restrict__ y, int y_bf16, int64_t y_stride) {
@@ -732,8 +733,8 @@ void run_few(const Product& a) {
 template <typename S, int MT, int RW, int KW>
 void run_rows(const Product& a) {
     const dim3 grid((unsigned)((a.w.n_out + 16 * RW - 1) / (16 * RW)), (unsigned)((a.rows + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL((k_matvec_rows<S, MT, RW, KW>), grid, dim3(64 * RW * KW), 0, a.s, a.w, static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y,
-                       a.y_bf16, a.y_stride);
+    hipLaunchKernelGGL((k_matvec_rows<S, MT, RW, KW>), grid, dim3(64 * RW * KW), 0, a.s, a.w,
+                       static_cast<const uint16_t*>(a.x.p), a.x.stride, a.rows, a.y, a.y_bf16, a.y_stride);
 }
 
 // S<SPAN>: what loads W, in spans of SPAN chunks. The choices were measured

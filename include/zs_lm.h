@@ -24,7 +24,8 @@
  * Logits, gradients of logits, x and y are row-major matrices whose rows start
  * `stride` elements apart (the row's length <= stride <= 2^38) and need only be
  * aligned to their elements; elements between a row's end and the next row's
- * start are neither read nor written. Calls over logits take up to 2^22 - 1 rows. fp32 and int32 arrays are contiguous and
+ * start are neither read nor written. Calls over logits take up to 2^22 - 1
+ * rows. fp32 and int32 arrays are contiguous and
  * 4-byte aligned, codes_all and scales_all 16-byte aligned.
  *
  * Sums, maxima and softmax statistics are held in fp32 or wider; a result is

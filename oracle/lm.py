@@ -1,5 +1,5 @@
 """Plain 64-bit implementations of the language-model operators, written from
-their definitions: the checker the tests compare the kernels with. Row by
+their definitions: the oracle the tests compare the kernels with. Row by
 row in numpy, no vector tricks shared with the library.
 """
 import math

@@ -1,5 +1,5 @@
 """Token log-probabilities, their gradient and top-logit distillation against
-the 64-bit checker (oracle/lm.py).
+the 64-bit oracle (oracle/lm.py).
 
 Tolerances, in units u = 2^-24 (half a step of fp32). An exponential e^d is off
 by 4 u |d| (the difference, the factor log2(e) / T and their product round) and

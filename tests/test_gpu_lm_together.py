@@ -4,7 +4,7 @@ log-probabilities with alternatives), is distilled from a teacher and pushed
 by a policy gradient, and the weight gradients go through the shard step of
 every rank into the next payload, from which the next tokens are answered.
 
-Each hand-over is checked against the 64-bit checker on what the operator
+Each hand-over is checked against the 64-bit oracle on what the operator
 before it really delivered, so that errors cannot hide in one another.
 """
 import math

@@ -1,4 +1,4 @@
-"""The 64-bit checker of the language-model operators against central
+"""The 64-bit oracle of the language-model operators against central
 differences and closed forms (no GPU)."""
 import math
 
