@@ -195,10 +195,11 @@ __device__ __forceinline__ void add_one(Running& r, float x, float k) {
     r.t += e * fmaxf(d, kLowest);
 }
 
-// The block's Running from its threads', the same in every thread. THREADS / 64
-// entries of `part`, which may be used again after the next barrier.
-template <int THREADS>
-__device__ __forceinline__ Running block_merge(Running r, float k, Running* part) {
+// The block's Running from its threads', the same in every thread; `part` may
+// be used again after the next barrier.
+template <int THREADS, int WAVES>
+__device__ __forceinline__ Running block_merge(Running r, float k, Running (&part)[WAVES]) {
+    static_assert(WAVES >= THREADS / 64, "an entry a wave");
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
         const Running o{__shfl_xor(r.m, d, 64), __shfl_xor(r.s, d, 64), __shfl_xor(r.t, d, 64)};
@@ -359,11 +360,20 @@ __device__ __forceinline__ Fast fast_running(Fast r, const T* row, int first, in
     return r;
 }
 
+// A block's sums, a wave each, of either form. The forms differ in size, so
+// the reductions take them as arrays whose length is checked.
+template <int WAVES>
+union BlockParts {
+    Running any[WAVES];
+    Fast fast[WAVES];
+};
+
 // The block's sums, the same in every thread: the maximum first, then each lane
-// moves its sums to it once. THREADS / 64 entries of `part`.
-template <int THREADS, bool ENTROPY>
-__device__ __forceinline__ Fast fast_block_merge(Fast r, float k, Fast* part) {
+// moves its sums to it once.
+template <int THREADS, bool ENTROPY, int WAVES>
+__device__ __forceinline__ Fast fast_block_merge(Fast r, float k, Fast (&part)[WAVES]) {
     constexpr int W = THREADS / 64;
+    static_assert(WAVES >= W, "an entry a wave");
     fast_rebase<ENTROPY>(r, wave_max(r.m), k);
     r.s = wave_sum(r.s);
     if (ENTROPY) r.t = wave_sum(r.t);
@@ -388,11 +398,9 @@ struct RowStats {
 };
 
 template <typename T, int THREADS, bool ENTROPY>
-__device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float k, Running* part) {
-    static_assert(sizeof(Fast) * (THREADS / 64) <= 1024, "part");
-    Fast* fpart = reinterpret_cast<Fast*>(part);
+__device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float k, BlockParts<THREADS / 64>& part) {
     const Fast own = fast_running<T, THREADS, ENTROPY, 4>(Fast{-kInf, 0.0f, 0.0f, 0.0f}, row, 0, vocab, k);
-    const Fast r = fast_block_merge<THREADS, ENTROPY>(own, k, fpart);
+    const Fast r = fast_block_merge<THREADS, ENTROPY>(own, k, part.fast);
     if (ordinary(r)) {
         // from c to the maximum: x k - c = (x - m) k + (m k - c)
         const float shift = __builtin_fmaf(r.m, k, -r.c);
@@ -400,7 +408,7 @@ __device__ __forceinline__ RowStats row_stats(const T* row, int64_t vocab, float
     }
     __syncthreads();  // every thread has read the block's parts
     const Running a = row_running<T, THREADS>(row, vocab, k);
-    const Running b = block_merge<THREADS>(a, k, part);
+    const Running b = block_merge<THREADS>(a, k, part.any);
     if (b.m == -kInf && b.s == 0.0f) return RowStats{-kInf, 0.0f, 0.0f, -kInf};
     if (!(b.s < kInf)) return RowStats{b.m, quiet_nan(), quiet_nan(), a.m};
     return RowStats{b.m, logf(b.s), b.t / b.s, a.m};
@@ -659,7 +667,7 @@ template <typename T, int THREADS, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logits, int64_t stride, int64_t vocab,
                                                       const int32_t* __restrict__ tokens, float inv_t, float k,
                                                       LogprobsOut out) {
-    __shared__ Running part[1024 / sizeof(Running)];
+    __shared__ BlockParts<THREADS / 64> part;
     __shared__ TopShared sh;
     const int64_t r = blockIdx.x;
     const T* row = logits + r * stride;
@@ -784,7 +792,7 @@ struct DistillShared {
     int32_t id[ZS_DISTILL_MAX_K];  // its tokens, -1 for unused entries
     int32_t slot[kSlots];
     int32_t repeated;
-    Running part[16];
+    BlockParts<1024 / 64> part;
 };
 
 // The teacher's side of a row: its largest logit, 1 / the sum of its
@@ -964,7 +972,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     }
     f = fast_running<T, THREADS, false, NV >= 16 ? 2 : 4>(f, row, NV * THREADS, vocab, k);
     if ((int)threadIdx.x < n) put(threadIdx.x, id, t, z);
-    f = fast_block_merge<THREADS, false>(f, k, reinterpret_cast<Fast*>(sh.part));  // its barrier publishes the entries
+    f = fast_block_merge<THREADS, false>(f, k, sh.part.fast);  // its barrier publishes the entries
     const TeacherStats ts = teacher_stats(n, vocab, k, sh);
     if (ts.bad || ts.max == -kInf) {
         const float fill = ts.bad ? quiet_nan() : 0.0f;
@@ -1005,7 +1013,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     }
     // any other row: differences from the maximum first, the row read again
     __syncthreads();
-    const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, sh.part);
+    const Running a = block_merge<THREADS>(row_running<T, THREADS>(row, vocab, k), k, sh.part.any);
     const float m = base_of(a.m);
     if (threadIdx.x < 64) {
         const float l = teacher_loss(n, ts, m, logf(a.s), inv_t, k, sh);
