@@ -129,7 +129,7 @@ zs_status zs_quant_matvec(const zs_plan* plan, int32_t tensor, int64_t out_featu
         const Span ys = matrix_span(y, rows, out_features, y_stride, y_esz);
         if (zs_status st = check_apart(ys, matrix_span(x_bf16, rows, in_features, x_stride, 2), "y", "x_bf16"))
             return st;
-        if (zs_status st = check_apart(ys, span(codes_all, plan->T * bits / 8), "y", "codes_all")) return st;
+        if (zs_status st = check_apart(ys, span(codes_all, plan->T / 8 * bits), "y", "codes_all")) return st;
         if (zs_status st = check_apart(ys, span(scales_all, 4 * n_scales * plan->world), "y", "scales_all")) return st;
     }
     zs::QuantWeight w{codes_all, scales_all, t.flat_off,  out_features, in_features,
