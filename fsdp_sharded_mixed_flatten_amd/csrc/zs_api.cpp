@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "zs_internal.h"
+#include "zs_lm_internal.h"
 
 namespace {
 
@@ -124,10 +125,6 @@ std::unordered_map<const void*, Binding> g_bind;
 
 // For the other host files of the library (zs_lm_internal.h).
 namespace zs {
-
-zs_status report(zs_status st, const char* fmt, ...);
-zs_status report_hip(int err, const char* what);
-void trace_call(const char* op, const zs_plan* p, int32_t n_contribs, int64_t off, int64_t len, const void* stream);
 
 zs_status report(zs_status st, const char* fmt, ...) {
     char buf[512];
