@@ -45,21 +45,39 @@ zs_status check_stride(int64_t stride, int64_t cols, const char* what) {
     return ZS_OK;
 }
 
+// The bytes of a matrix (or, as one row, of an array): [lo, lo + row), again
+// every `stride` bytes, up to hi. Empty where lo == hi.
 struct Span {
-    uintptr_t lo, hi;  // [lo, hi) bytes; empty where lo == hi
+    uintptr_t lo, hi;
+    uintptr_t row, stride;  // stride 0: one row
 };
 
 Span span(const void* p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Span{a, p ? a + (uintptr_t)bytes : a};
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), n = p ? (uintptr_t)bytes : 0;
+    return Span{a, a + n, n, 0};
 }
 
 Span matrix_span(const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t esz) {
-    return span(p, rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * esz : 0);
+    if (rows <= 1 || cols == 0) return span(p, rows > 0 ? cols * esz : 0);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Span{a, a + (uintptr_t)(((rows - 1) * stride + cols) * esz), (uintptr_t)(cols * esz),
+                (uintptr_t)(stride * esz)};
 }
 
-zs_status check_apart(Span a, Span b, const char* what_a, const char* what_b) {
-    if (a.lo < b.hi && b.lo < a.hi) return report(ZS_EINVAL, "%s overlaps %s", what_a, what_b);
+// Whether no byte belongs to both. Exact for rows that repeat at one distance
+// (columns of one matrix side by side, an array between two rows); matrices of
+// different strides have to lie in ranges apart.
+bool apart(const Span& a, const Span& b) {
+    if (!(a.lo < b.hi && b.lo < a.hi)) return true;
+    const uintptr_t stride = a.stride ? a.stride : b.stride;
+    if (stride == 0 || (b.stride && b.stride != stride)) return false;
+    // how far b's rows start behind a's, modulo the stride
+    const uintptr_t d = b.lo >= a.lo ? (b.lo - a.lo) % stride : (stride - (a.lo - b.lo) % stride) % stride;
+    return d >= a.row && b.row <= stride - d;
+}
+
+zs_status check_apart(const Span& a, const Span& b, const char* what_a, const char* what_b) {
+    if (!apart(a, b)) return report(ZS_EINVAL, "%s overlaps %s", what_a, what_b);
     return ZS_OK;
 }
 
@@ -216,7 +234,7 @@ zs_status zs_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64
         if (zs_status st = check_grad(logits, dtype, rows, vocab, row_stride, grad_logits, grad_stride)) return st;
     const int64_t esz = elem_bytes(dtype);
     const Span l = span(loss, 4 * rows);
-    const Span g = grad_logits ? matrix_span(grad_logits, rows, vocab, grad_stride, esz) : Span{0, 0};
+    const Span g = grad_logits ? matrix_span(grad_logits, rows, vocab, grad_stride, esz) : span(nullptr, 0);
     const Span in[3] = {span(teacher_ids, 4 * rows * k), span(teacher_logits, 4 * rows * k),
                         span(row_weight, 4 * rows)};
     const char* in_name[3] = {"teacher_ids", "teacher_logits", "row_weight"};

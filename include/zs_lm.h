@@ -26,7 +26,10 @@
  * aligned to their elements; elements between a row's end and the next row's
  * start are neither read nor written. Calls over logits take up to 2^22 - 1
  * rows. fp32 and int32 arrays are contiguous and
- * 4-byte aligned, codes_all and scales_all 16-byte aligned.
+ * 4-byte aligned, codes_all and scales_all 16-byte aligned. Buffers that may
+ * not overlap may still lie between each other's rows, as columns of one matrix
+ * do; two matrices whose rows start different numbers of bytes apart have to
+ * lie in address ranges apart.
  *
  * Sums, maxima and softmax statistics are held in fp32 or wider; a result is
  * rounded once, when it is stored.

@@ -99,6 +99,96 @@ void largest_products() {
     CHECK(zs::g_launches == before + 2);
 }
 
+// Buffers that share an address range and no element are accepted (columns side
+// by side in one matrix, an array between two rows), buffers that share one
+// byte are not. Rows of 100 elements, 4 of them.
+void neighbours() {
+    const uint64_t a = uint64_t(1) << 40, far = uint64_t(1) << 50;
+    auto* tok = at<int32_t>(far);
+    auto* f = at<float>(far + (1 << 20));
+    auto grad = [&](uint64_t z, int64_t zs, uint64_t g, int64_t gs, int dtype, int64_t rows = 4) {
+        return zs_token_logprobs_backward(at(z), dtype, rows, 100, zs, tok, 1.0f, f, nullptr, f, nullptr, at(g), gs,
+                                          nullptr);
+    };
+    for (int dtype : {ZS_DTYPE_BF16, ZS_DTYPE_F32}) {
+        const uint64_t e = dtype == ZS_DTYPE_BF16 ? 2 : 4;
+        CHECK(grad(a, 200, a + 100 * e, 200, dtype) == ZS_OK);          // right half
+        CHECK(grad(a + 100 * e, 200, a, 200, dtype) == ZS_OK);          // left half
+        CHECK(grad(a, 203, a + 103 * e, 203, dtype) == ZS_OK);
+        CHECK(grad(a, 200, a + 99 * e, 200, dtype) == ZS_EINVAL);       // an element too far left
+        CHECK(grad(a, 200, a + 101 * e, 200, dtype) == ZS_EINVAL);      // an element too far right
+        CHECK(grad(a, 200, a + (3 * 200 + 100) * e, 200, dtype) == ZS_OK);
+        CHECK(grad(a, 200, a + (2 * 200 + 100) * e, 200, dtype) == ZS_OK);
+        CHECK(grad(a, 200, a + 2 * 200 * e, 200, dtype) == ZS_EINVAL);  // two rows further on
+        CHECK(grad(a, 200, a + 100 * e, 201, dtype) == ZS_EINVAL);      // halves that drift into each other
+        CHECK(grad(a, 300, a + 100 * e, 500, dtype, 1) == ZS_OK);       // one row: its stride says nothing
+        CHECK(grad(a, 300, a + 99 * e, 500, dtype, 1) == ZS_EINVAL);
+        // distillation: loss and entries between the rows of a gradient
+        auto distill = [&](uint64_t loss, uint64_t ids) {
+            return zs_distill_topk(at(a + 100 * e), dtype, 4, 100, 300, at<int32_t>(ids), f, 2, 1.0f, nullptr,
+                                   at<float>(loss), at(a), 300, nullptr);
+        };
+        CHECK(distill(a + 200 * e, a + (300 + 200) * e) == ZS_OK);
+        CHECK(distill(a + 300 * e - 16, far) == ZS_OK);
+        CHECK(distill(a + 300 * e - 12, far) == ZS_EINVAL);
+        CHECK(distill(a + 200 * e - 4, far) == ZS_EINVAL);
+        CHECK(distill(far + (1 << 24), a + 300 * e - 32) == ZS_OK);
+        CHECK(distill(far + (1 << 24), a + 300 * e - 28) == ZS_EINVAL);
+        CHECK(distill(a + 200 * e, a + 200 * e + 12) == ZS_EINVAL);  // and between themselves
+    }
+    // log-probabilities: tokens and outputs behind the logits of each row
+    auto scored = [&](uint64_t lp, uint64_t st) {
+        return zs_token_logprobs(at(a), ZS_DTYPE_F32, 4, 100, 164, tok, 1.0f, at<float>(lp), nullptr, at<float>(st), 0,
+                                 nullptr, nullptr, nullptr);
+    };
+    CHECK(scored(a + 400, a + 416) == ZS_OK);
+    CHECK(scored(a + 400, a + 412) == ZS_EINVAL);
+    CHECK(scored(a + 396, far + 4096) == ZS_EINVAL);
+    CHECK(scored(a + 656 - 16, a + 656 - 48) == ZS_OK);
+    CHECK(scored(a + 656 - 12, far + 4096) == ZS_EINVAL);
+    // products: x and y columns of one matrix, in bf16 and with fp32 results
+    const PlanOf plan({24 * 48}, 2, 8);
+    auto product = [&](uint64_t x, int64_t xs, uint64_t y, int64_t ys, int dtype) {
+        return zs_quant_matvec(plan.p, 0, 24, 48, 4, 8, at(far), at<float>(far + (1 << 20)), at(x), xs, 5, at(y), dtype,
+                               ys, nullptr);
+    };
+    CHECK(product(a, 72, a + 96, 72, ZS_DTYPE_BF16) == ZS_OK);
+    CHECK(product(a + 48, 72, a, 72, ZS_DTYPE_BF16) == ZS_OK);
+    CHECK(product(a, 72, a + 94, 72, ZS_DTYPE_BF16) == ZS_EINVAL);
+    CHECK(product(a, 96, a + 96, 48, ZS_DTYPE_F32) == ZS_OK);
+    CHECK(product(a, 96, a + 100, 48, ZS_DTYPE_F32) == ZS_EINVAL);
+    CHECK(product(a, 96, a + 96, 96, ZS_DTYPE_F32) == ZS_EINVAL);  // rows of other lengths in bytes
+}
+
+// x and y of a product at random places and strides against their bytes one by
+// one: nothing that overlaps is accepted, and at one distance of rows nothing
+// else is refused.
+void neighbours_at_random(std::mt19937_64& rng) {
+    const int64_t out = 3, in = 5;
+    const PlanOf plan({out * in}, 1, 1);
+    const uint64_t far = uint64_t(1) << 50, base = uint64_t(1) << 40;
+    int accepted = 0, refused = 0;
+    for (int i = 0; i < 100000; ++i) {
+        const int32_t rows = 1 + (int32_t)(rng() % 4), dtype = (int32_t)(rng() % 2);
+        const int64_t e = dtype == ZS_DTYPE_BF16 ? 2 : 4, xs = in + (int64_t)(rng() % 8);
+        const int64_t ys = rng() % 2 && (xs * 2) % e == 0 && xs * 2 / e >= out ? xs * 2 / e : out + (int64_t)(rng() % 8);
+        const uint64_t x = base + 2 * (rng() % 64), y = base + (uint64_t)e * (rng() % 32);
+        bool touch = false;
+        for (int64_t r = 0; r < rows; ++r)
+            for (int64_t q = 0; q < rows; ++q) {
+                const uint64_t xr = x + (uint64_t)(r * xs * 2), yr = y + (uint64_t)(q * ys * e);
+                touch = touch || (xr < yr + (uint64_t)(out * e) && yr < xr + (uint64_t)(in * 2));
+            }
+        const zs_status st = zs_quant_matvec(plan.p, 0, out, in, 4, 8, at(far), at<float>(far + 4096), at(x), xs, rows,
+                                             at(y), dtype, ys, nullptr);
+        CHECK(st == ZS_OK || st == ZS_EINVAL);
+        CHECK(!touch || st == ZS_EINVAL);
+        if (xs * 2 == ys * e || rows == 1) CHECK(touch == (st == ZS_EINVAL));
+        ++(st == ZS_OK ? accepted : refused);
+    }
+    CHECK(accepted > 1000 && refused > 1000);
+}
+
 // Random arguments around the limits: a call that is accepted launches once or
 // has nothing to do, any other leaves a text.
 void random_calls(std::mt19937_64& rng, int count, const zs_plan* plan) {
@@ -167,8 +257,10 @@ int main(int argc, char** argv) {
     if (mode == "all") {
         largest_extents();
         largest_products();
+        neighbours();
         const PlanOf plan({24, 48}, 2, 8);
         std::mt19937_64 rng(1);
+        neighbours_at_random(rng);
         random_calls(rng, 200000, plan.p);
     }
     concurrent_callers();
