@@ -18,7 +18,8 @@ WHOLE = [
     (8192, 256, 2, 0, 256, (32, 256)),
     (8193, 256, 1, 256, 256, (64, 128)),
     (32767, 256, 1, 0, 256, (32, 256)),
-    (32768, 256, 8, 256, 256, (128,)),
+    (32768, 256, 8, 256, 256, (128,)),       # shards that end inside a block: split
+    (32784, 256, 2, 0, 256, (128,)),
     (32771, 256, 1, 0, 256, (64, 256)),
     (33000, 96, 1, 96, 32, (32,)),          # a row ends inside a chunk
     (4112, 2304, 2, 0, 256, (32, 64, 256)),  # more than 2048 columns: turns for every wave
