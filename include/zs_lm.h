@@ -63,8 +63,11 @@ typedef enum zs_dtype { ZS_DTYPE_BF16 = 0, ZS_DTYPE_F32 = 1 } zs_dtype;
  * the memory's speed where tensor offset, in_features and shard length are
  * multiples of block and block >= 32, slower where they are not, and slowest
  * with smaller blocks. A block whose
- * scale is NaN (an infinity or NaN among its parameters) gives NaN, and an
- * infinity or NaN in x gives infinities or NaN in its row of y.
+ * scale is NaN (an infinity or NaN among its parameters) gives NaN in the rows
+ * of W that have elements in it, and an infinity or NaN in x gives infinities
+ * or NaN in its row of y. Codes are multiplied with x and summed over up to 128
+ * columns before the scale: |x| up to 2^122 (4 bits) or 2^114 (8 bits) cannot
+ * overflow there, larger values may give infinities or NaN in their row of y.
  *
  * FLAT plans. bits 4 or 8. out_features <= 2^25, in_features <= 2^29. x is bf16, y bf16 or fp32 (y_dtype).
  * 0 <= rows <= ZS_QUANT_MATVEC_MAX_ROWS (more rows: dequantize once and use a
