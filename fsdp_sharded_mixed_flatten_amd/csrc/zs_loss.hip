@@ -5,9 +5,10 @@
 // Every kernel is a stream over rows of `vocab` logits (2 or 4 bytes each)
 // with one exponential and a few fp32 operations an element. Differences
 // from the row's maximum are taken of the logits themselves, before the
-// temperature scales them, so values near the type's ends neither overflow nor
-// lose their order; exponentials are powers of two of differences scaled by
-// log2(e) / temperature.
+// temperature scales them; exponentials are powers of two of differences scaled
+// by log2(e) / temperature. A difference of more than fp32's largest value is
+// -infinity and its exponential the 0 that it is; outputs that are differences
+// over the temperature, and may be finite then, take halves (quotient()).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -28,6 +29,12 @@ constexpr float kLn2 = 0.693147180559945309f;
 // Differences d are bounded below by this where they multiply 2^d, which is 0
 // long before (and the products stay far from infinity).
 constexpr float kLowest = -1.0e4f;
+
+// (x - m) / temperature. Halves differ by no more than fp32's largest value, and
+// halving is exact.
+__device__ __forceinline__ float quotient(float x, float m, float inv_t) {
+    return (0.5f * x - 0.5f * m) * (2.0f * inv_t);
+}
 
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
 
@@ -650,7 +657,7 @@ __device__ __forceinline__ void row_outputs(int64_t r, const RowStats& st, float
     if (threadIdx.x == 0) {
         // m is -infinity in a row of nothing else and in one with a NaN beside (log s is NaN)
         const bool masked = st.m == -kInf && st.logsum == 0.0f && x == -kInf;
-        if (out.logprob) out.logprob[r] = masked ? -kInf : (x - st.m) * inv_t - st.logsum;
+        if (out.logprob) out.logprob[r] = masked ? -kInf : quotient(x, st.m, inv_t) - st.logsum;
         if (out.entropy) out.entropy[r] = st.logsum - kLn2 * st.mean_d;
         if (out.stats) {
             out.stats[2 * r] = st.m;
@@ -682,7 +689,7 @@ __global__ __launch_bounds__(THREADS) void k_logprobs(const T* __restrict__ logi
     if (out.top == 0 || !(st.logsum < kInf)) return;
     top_elements<T, THREADS>(row, vocab, out.top, st.own, sh, [&](int place, float x, int id) {
         out.top_ids[r * out.top + place] = id;
-        out.top_logprobs[r * out.top + place] = st.m == -kInf ? -kInf : (x - st.m) * inv_t - st.logsum;
+        out.top_logprobs[r * out.top + place] = st.m == -kInf ? -kInf : quotient(x, st.m, inv_t) - st.logsum;
     });
 }
 
@@ -818,15 +825,20 @@ __device__ __forceinline__ TeacherStats teacher_stats(int n, int64_t vocab, floa
     return TeacherStats{m, 1.0f / s, logf(s), (bool)__any(bad)};
 }
 
-// loss / T^2 = sum of q ((t - max) / T - (x - m) / T + log s - log sum of the
-// teacher's exponentials); one wave.
+// Losses are summed in units of 2^24: a difference of two logits over the
+// smallest temperature is below 2^150, and in units of 2^24 in fp32's range.
+constexpr float kLossUnit = 16777216.0f;
+
+// loss / T^2 in that unit = sum of q ((t - max) / T - (x - m) / T + log s - log
+// sum of the teacher's exponentials); one wave.
 __device__ __forceinline__ float teacher_loss(int n, const TeacherStats& ts, float m, float logsum, float inv_t,
                                               float k, const DistillShared& sh) {
     float l = 0.0f;
     for (int i = threadIdx.x & 63; i < n; i += 64) {
         const float dt = sh.t[i] - ts.max;
         const float q = exp2f(dt * k) * ts.inv;
-        if (q > 0.0f) l += q * ((dt - (sh.x[i] - m)) * inv_t + (logsum - ts.logsum));
+        const float half = 0.5f * dt - (0.5f * sh.x[i] - 0.5f * m);
+        if (q > 0.0f) l += q * (half * (inv_t * (2.0f / kLossUnit)) + (logsum - ts.logsum) * (1.0f / kLossUnit));
     }
     return wave_sum(l);
 }
@@ -984,7 +996,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     if (ordinary(f)) {
         if (threadIdx.x < 64) {
             const float l = teacher_loss(n, ts, f.m, logf(f.s) - kLn2 * __builtin_fmaf(f.m, k, -f.c), inv_t, k, sh);
-            if (threadIdx.x == 0) loss[r] = w * temperature * temperature * l;
+            if (threadIdx.x == 0) loss[r] = w * temperature * temperature * kLossUnit * l;
         }
         if (!grad) return;
         find_repeated<THREADS>(n, sh);
@@ -1017,7 +1029,8 @@ __global__ __launch_bounds__(THREADS) void k_distill(const T* logits, int64_t st
     const float m = base_of(a.m);
     if (threadIdx.x < 64) {
         const float l = teacher_loss(n, ts, m, logf(a.s), inv_t, k, sh);
-        if (threadIdx.x == 0) loss[r] = w * temperature * temperature * (a.m == -kInf && a.s == 0.0f ? kInf : l);
+        const bool masked = a.m == -kInf && a.s == 0.0f;
+        if (threadIdx.x == 0) loss[r] = w * temperature * temperature * kLossUnit * (masked ? kInf : l);
     }
     if (!grad) return;
     find_repeated<THREADS>(n, sh);
