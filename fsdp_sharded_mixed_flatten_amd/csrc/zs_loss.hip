@@ -1064,16 +1064,19 @@ void run_logprobs(Rows logits, int64_t rows, int64_t vocab, const int32_t* token
 int launch_logprobs(Rows logits, int dtype, int64_t rows, int64_t vocab, const int32_t* tokens, double temperature,
                     const LogprobsOut& out, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    // 512 threads a row where rows are few or 128 KB and longer, else 256 (8
-    // alternatives; 512 threads against 256, us: 64 x 151936 fp32 16.5, 23.2;
-    // 4096 x 128256 bf16 189, 199; 4096 x 65536 bf16 102, 105; 4096 x 32000 fp32
-    // 95, 102; the other way round 4096 x 32000 bf16 70, 55; 4096 x 8192 bf16 50,
-    // 21; about even at 512 rows of 128256 and 32000)
-    const int64_t row_bytes = vocab * (dtype == ZS_DTYPE_BF16 ? 2 : 4);
-    const bool wide = vocab > 8192 && (rows <= 1024 || row_bytes >= 128000);
-    if (dtype == ZS_DTYPE_BF16 && wide)
+    // 512 threads a row where rows are few or long, else 256. With 8
+    // alternatives, 256 threads against 512, us: few rows 64 x 151936 fp32 23.2,
+    // 16.5; about even at 512 rows of 128256 and 32000 bf16. 4096 rows of bf16:
+    // 32768 53, 67; 49152 78, 82; 57344 90, 102; 65536 (128 KB) 104, 98; 81920 127,
+    // 119. 4096 rows of fp32: 16384 52, 50; 20480 65, 64; 24576 (96 KB) 76, 72;
+    // 28672 88, 83; 32768 101, 94. Without alternatives 512 threads gain 1 to 5%
+    // from these lengths on.
+    const bool bf16 = dtype == ZS_DTYPE_BF16;
+    const int64_t row_bytes = vocab * (bf16 ? 2 : 4);
+    const bool wide = vocab > 8192 && (rows <= 1024 || row_bytes >= (bf16 ? 128 << 10 : 96 << 10));
+    if (bf16 && wide)
         run_logprobs<uint16_t, 512>(logits, rows, vocab, tokens, temperature, out, s);
-    else if (dtype == ZS_DTYPE_BF16)
+    else if (bf16)
         run_logprobs<uint16_t, 256>(logits, rows, vocab, tokens, temperature, out, s);
     else if (wide)
         run_logprobs<float, 512>(logits, rows, vocab, tokens, temperature, out, s);
