@@ -11,6 +11,7 @@
 // over the temperature, and may be finite then, take halves (quotient()).
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -518,8 +519,10 @@ __device__ __forceinline__ void top_by_rounds(const T* row, int64_t vocab, int t
 // come from a cache), those that reach it are listed, and the list is ranked by
 // counting. The second reading is dealt out over the whole block: left to the
 // threads themselves it was a chain of loads a few lanes wide. A
-// row with more of them than the list holds (equal logits, most of the
-// vocabulary masked, an order by size) goes by rounds.
+// row with more of them than the list holds (equal logits, an order by size)
+// goes by rounds. Where fewer than `top` groups hold a logit above -infinity (most
+// of the vocabulary is masked), all that are above it are listed (10 tokens of
+// 128256 allowed, 20 alternatives, bf16: 17 us for one row; by rounds 347).
 constexpr int kListed = 512;
 struct TopShared {
     float group[64];
@@ -567,6 +570,13 @@ __device__ __forceinline__ void top_rank(const T* row, int64_t vocab, int top, T
     }
     if (n <= 64) {  // the usual list: one wave, an entry a lane
         if (threadIdx.x >= 64) return;
+        if (n < top) {
+            // every logit above -infinity is listed: the places left go to the
+            // lowest masked tokens, which are among the first `top`
+            const bool masked = lane < top && Vec<T>::one(row[lane]) == -kInf;
+            const int at = n + (int)__popcll(__ballot(masked) & ((1ull << lane) - 1));
+            if (masked && at < top) put(at, -kInf, lane);
+        }
         const uint64_t key = sh.key[lane];
         int place = 0;
         for (int o = 0; o < n; ++o) {
@@ -589,7 +599,7 @@ __device__ __forceinline__ void top_rank(const T* row, int64_t vocab, int top, T
 template <typename T, int THREADS, typename Put>
 __device__ __forceinline__ void top_elements(const T* row, int64_t vocab, int top, float own, TopShared& sh, Put put) {
     constexpr int N = Vec<T>::kN;
-    const float bound = top_bound<THREADS>(top, own, sh);
+    const float bound = fmaxf(top_bound<THREADS>(top, own, sh), -FLT_MAX);
     const int64_t nv = vocab / N;
     if (own >= bound) {
         sh.owner[atomicAdd(&sh.owners, 1)] = threadIdx.x;
