@@ -1150,7 +1150,7 @@ int pick_distill(Rows logits, int64_t rows, int64_t vocab, const Teacher& t, dou
                  void* grad, int64_t grad_stride, hipStream_t s) {
     // As many threads and vectors a thread as hold the row; 20 vectors are what
     // 1024 threads have registers for (4096 x 151936 bf16, 19 vectors: 487 us,
-    // read twice 549; 1024 x 151936 fp32, 20 of 38 held: 271 us against 330).
+    // read twice 549; 1024 x 151936 fp32, 20 of 38 held: 271 us against 330, 252 now).
     const int64_t nv = vocab / Vec<T>::kN;  // 16-byte vectors of a row
     if (nv <= 256 * 4)
         run_distill<T, 256, 4>(logits, rows, vocab, t, temperature, loss, grad, grad_stride, s);

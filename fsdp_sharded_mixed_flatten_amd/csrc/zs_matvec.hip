@@ -50,6 +50,10 @@ __device__ __forceinline__ float wave_sum(float v) {
 // of 8 of a shard), so it has one scale and its codes are one aligned 32- or
 // 64-bit word. The units at the row's ends may reach into the neighbouring
 // tensors; their elements there are left out.
+// 8192 x 8192 int4 in blocks of 8 takes 18 us with one row of x, 28 with 4, 94
+// with 16 and 350 with 64 (67 MB, 10.5 us at 6.4 TB/s); blocks of 16 with one row
+// 18 and with 4 28 (50 MB, 7.9 us). An fp32 multiply-add a weight and row, every
+// unit's loads waited for before the next, and W read again for every 4 rows.
 constexpr int kAnyWaves = 4;
 
 template <int BITS, int M>
@@ -159,7 +163,11 @@ void run_any(const QuantWeight& w, Rows x, int rows, void* y, bool y_bf16, int64
 // 16-byte loads) and the next span's before it computes a span. Plain loads:
 // a row's 64 bytes of a chunk are half a cache line, and with the nontemporal
 // hint the line's other half came from memory again (28672 x 8192 int4, one
-// row of x: 31.6 against 24.5 us).
+// row of x: 30.5 against 26.9 us).
+//
+// Times in this file are of calls on three sets of inputs in turn, unless they
+// say one set: 125 MB of codes used again at once are partly held by the last
+// cache (the 26.9 us are then 24.1).
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -342,8 +350,9 @@ struct Span {
 // its 32 codes and shifts them into place. Lane (g, r) works out boundary and
 // scales of row r in window g of a chunk; the other lane groups ask it for them.
 // More than twice the arithmetic and loads of whole blocks, which bound it: 8191
-// x 8191 int4, blocks of 128, takes 26 us with one row of x and 39 with 16 (8192
-// x 8192 in whole blocks 12 and 16; k_matvec_any 26 and 174).
+// x 8191 int4, blocks of 128, takes 24 us with one row of x, 28 with 4 and 16 and
+// 67 with 64 (8192 x 8192 in whole blocks 10, 13, 15 and 29; k_matvec_any 21, 49,
+// 165 and 633: with one row alone it is ahead).
 template <int BITS, int SPAN_>
 struct SplitSpan {
     static constexpr int SPAN = SPAN_, kBits = BITS;
@@ -489,12 +498,12 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t* x, int k, int n_in) {
 // span's columns of each row once, contiguously, and its lanes read their
 // operands from there (loading operands straight from x issues 4 wide loads a
 // chunk that mostly repeat each other, and took 36 instead of 24.5 us at 28672
-// x 8192 int4). The waves of a workgroup share its 16 rows of W and take turns
-// over the spans; their sums meet in shared memory at the end.
-// Reads at 4.7 TB/s at 28672 x 8192 int4 (26.6 us, one row), 5.2 TB/s at 8192 x
+// x 8192 int4, one set of inputs). The waves of a workgroup share its 16 rows of
+// W and take turns over the spans; their sums meet in shared memory at the end.
+// Reads at 4.6 TB/s at 28672 x 8192 int4 (26.9 us, one row), 5.2 TB/s at 8192 x
 // 128256 int8 (210 us, 4 rows, blocks of 128, fp32 results); bound by memory
-// there and by latency in products of a few MB (4096 x 4096 int4 4.6 us, an
-// empty launch 1.6 us).
+// there and by latency in products of a few MB (4096 x 4096 int4 4.0 us in a
+// captured graph, an empty launch 1.6 us).
 template <typename S, int ROWS>
 __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_t* __restrict__ x, int64_t x_stride,
                                                     int rows, void* __restrict__ y, int y_bf16, int64_t y_stride) {
@@ -597,7 +606,10 @@ __global__ __launch_bounds__(512) void k_matvec_few(QuantWeight w, const uint16_
 // into the other half of the buffer.
 // 28672 x 8192 int4 with 16 rows: 43 us against 76 with each wave loading its
 // own operands, 64 rows 97 against 258; at 2048 x 11008 with 16 rows 9.2
-// against 10.8.
+// against 10.8 (one set of inputs, an earlier form; 45, 102 and 8.8 us with
+// three sets now). Far from memory's speed, 2.8 TB/s with 16 rows and 1.2 with
+// 64: vector instructions take 17 and 50 us of these, shared memory 6 and 24, and
+// the waves wait half of their time.
 template <typename S, int MT, int RW, int KW>
 __global__ __launch_bounds__(64 * RW * KW) void k_matvec_rows(QuantWeight w, const uint16_t* __restrict__ x,
                                                               int64_t x_stride, int rows, void* __restrict__ y,
@@ -721,8 +733,8 @@ void run_few(const Product& a) {
     constexpr int kSpan = S::SPAN * kChunk;
     const int64_t tiles = (a.w.n_out + 15) / 16, spans = (a.w.n_in + kSpan - 1) / kSpan;
     // 8 waves a workgroup while a workgroup a CU is about all there is (4096 x
-    // 4096 int4 4.8 us against 5.4 with 4), else 4 (28672 x 8192 int4 24.4 us
-    // against 26.5 with 8, 8192 x 128256 114 against 147)
+    // 4096 int4 4.0 us against 4.4 with 4), else 4 (28672 x 8192 int4 26.9 us
+    // against 28.3 with 8, 8192 x 128256 107 against 152)
     const int most = tiles <= 256 ? 8 : 4;
     const int waves = spans < most ? (int)spans : most;
     const size_t lds = (size_t)waves * ROWS * (kSpan / 8 + 4) * 16 + (size_t)(waves - 1) * 64 * 4;
@@ -740,7 +752,7 @@ void run_rows(const Product& a) {
 // S<SPAN>: what loads W, in spans of SPAN chunks. The choices were measured
 // against each other (1 to 4 tiles of x, 1 to 8 waves that share it, 1 to 16
 // groups that split the columns, spans of 1 to 4) at the sizes in the comments
-// (columns x rows of W), int4, in us.
+// (columns x rows of W), int4, in us, one set of inputs.
 template <template <int> class S>
 void run_block(const Product& a) {
     constexpr bool kSplit = S<1>::kRagged;
@@ -830,7 +842,8 @@ int launch_quant_matvec(const QuantWeight& w, Rows x, int rows, void* y, int y_d
     const bool whole = w.off % block == 0 && w.n_in % block == 0 && w.shard % block == 0;
     // split blocks: at most one shard's end in a row, and no more than two
     // boundaries inside 32 columns (whole blocks of 16 have one: 8192 x 8192 int4
-    // with 16 rows 41 us against 94 a wave a row, with one 31 against 23)
+    // with 16 rows 28 us against 97 a wave a row, with 5 28 against 43, with 4 30
+    // against 28, with one 29 against 18)
     const bool split = w.shard >= w.n_in && (block >= 32 || (block == 16 && whole && rows > 4));
     if (block >= 32 && w.n_in > 0 && whole) {
         switch (w.block_shift) {
