@@ -1,8 +1,8 @@
 """Python binding of ``libzs.so``, the MI355X shard-local step (ZeRO / FSDP).
 
 Argument marshalling only: every step of the path runs in the library's HIP
-kernels. Functions carry the C ABI's names (``include/zs.h``, ``include/zs_lm.h``). Device buffers
-are PyTorch CUDA tensors (or raw integer device addresses); the stream is
+kernels. Functions carry the C ABI's names (``include/zs.h``, ``include/zs_clip.h``, ``include/zs_lm.h``,
+``include/zs_mx4.h``, ``include/zs_drafts.h``). Device buffers are PyTorch CUDA tensors (or raw integer device addresses); the stream is
 ``torch.cuda.current_stream()`` unless one is given. Before each call the
 binding checks that every tensor is a contiguous CUDA tensor of the right
 dtype and at least as long as the kernels will touch, so a wrong shape is a
@@ -26,6 +26,8 @@ ZS_DTYPE_BF16, ZS_DTYPE_F32 = 0, 1
 ZS_QUANT_MATVEC_MAX_ROWS = 64
 ZS_LOGPROBS_MAX_TOP = 32
 ZS_DISTILL_MAX_K = 1024
+ZS_MX4_BLOCK = 32
+ZS_VERIFY_MAX_DRAFTS = 64
 GRAD_STATS_NOALLOC_MAX_ELEMS = 1431568384
 FUSED_TWO_PASS_MIN_CONTRIBS = 52  # zs_fused_shard_step runs two passes from here when grad is given
 
@@ -152,6 +154,15 @@ def _load():
         "zs_token_logprobs": (st, [vp, i32, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, i32, vp, vp, vp]),
         "zs_token_logprobs_backward": (st, [vp, i32, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, i64, vp]),
         "zs_distill_topk": (st, [vp, i32, i64, i64, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64, vp]),
+        "zs_mx4_quantize": (st, [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]),
+        "zs_mx4_dequantize": (st, [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]),
+        "zs_mx4_matmul": (st, [vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]),
+        "zs_verify_drafts_workspace_bytes": (i64, [i64, i32, i64]),
+        "zs_verify_drafts": (st, [vp, i32, i64, i32, i64, i64, vp, i64, vp, vp, vp, ctypes.c_double, vp, vp, vp, vp,
+                                  i64, vp]),
+        "zs_grad_stats_multi_workspace_bytes": (i64, [vp]),
+        "zs_grad_stats_multi": (st, [vp, vp, vp, vp, vp, i64, vp]),
+        "zs_adamw_shard_step_multi_clip": (st, [vp, ctypes.POINTER(AdamWHParams), i32, vp, vp, vp, vp]),
         "zs_last_error": (ctypes.c_char_p, []),
         "zs_version": (ctypes.c_char_p, []),
     }
@@ -182,6 +193,10 @@ EXPORTED = ("zs_shard_plan", "zs_shard_plan_ex", "zs_plan_tensor_group", "zs_pla
             "zs_fused_shard_step_multi_dc", "zs_last_error", "zs_version")
 # the language-model operators (include/zs_lm.h)
 EXPORTED_LM = ("zs_quant_matvec", "zs_token_logprobs", "zs_token_logprobs_backward", "zs_distill_topk")
+# the microscaled 4-bit format, the verification of drafted tokens and the clipped multi-tensor step
+EXPORTED_MX4 = ("zs_mx4_quantize", "zs_mx4_dequantize", "zs_mx4_matmul")
+EXPORTED_DRAFTS = ("zs_verify_drafts_workspace_bytes", "zs_verify_drafts")
+EXPORTED_CLIP = ("zs_grad_stats_multi_workspace_bytes", "zs_grad_stats_multi", "zs_adamw_shard_step_multi_clip")
 
 
 def lib():
@@ -669,6 +684,30 @@ def zs_adamw_shard_step_accum(plan, hp, acc, grad_divisor, master, m, v, scale=N
                                           _ptr(full, "bf16", (r + 1) * S, "full"), _stream(stream)))
 
 
+def zs_grad_stats_multi_workspace_bytes(plan):
+    return _lib.zs_grad_stats_multi_workspace_bytes(plan.handle)
+
+
+def zs_grad_stats_multi(plan, sumsq_out, nonfinite_out, workspace, stats_workspace, stream=None):
+    """Squared norm and non-finite flag of the grad pieces bound to workspace.
+    sumsq_out: CUDA float64 tensor (>= 1 element); nonfinite_out: CUDA int32
+    tensor; stats_workspace: CUDA uint8 tensor of
+    zs_grad_stats_multi_workspace_bytes."""
+    _check(_lib.zs_grad_stats_multi(plan.handle, workspace.data_ptr(), _scalar_ptr(sumsq_out, "float64", "sumsq_out"),
+                                    _scalar_ptr(nonfinite_out, "int32", "nonfinite_out"),
+                                    _ptr(stats_workspace, "bytes", 0, "stats_workspace"), stats_workspace.numel(),
+                                    _stream(stream)))
+
+
+def zs_adamw_shard_step_multi_clip(plan, hps, workspace, scale=None, skip=None, stream=None):
+    """The multi-tensor AdamW step from the gradient times *scale, left out
+    where *skip is set. hps: one set of hyperparameters per group."""
+    arr, n = _hp_array(hps)
+    _check(_lib.zs_adamw_shard_step_multi_clip(plan.handle, arr, n, _scalar_ptr(scale, "float32", "scale"),
+                                               _scalar_ptr(skip, "int32", "skip"), workspace.data_ptr(),
+                                               _stream(stream)))
+
+
 # ---------------------------------------------------------------- scalars in device memory
 
 
@@ -903,6 +942,107 @@ def zs_distill_topk(logits, teacher_ids, teacher_logits, loss, grad_logits=None,
              _lm_array(teacher_logits, f32, rows * k, k, device, "teacher_logits"), k, temperature,
              _lm_array(row_weight, f32, rows, 0, device, "row_weight"),
              _lm_array(loss, f32, rows, 0, device, "loss"), gp, gs)
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floating point
+
+
+def _float_code(t, what):
+    if t.dtype is _torch.bfloat16:
+        return ZS_DTYPE_BF16
+    if t.dtype is _torch.float32:
+        return ZS_DTYPE_F32
+    raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _mx4_matrix(codes, scales, rows, blocks, device, names):
+    """(codes address, stride, scales address, stride) of a quantized [rows, 32 * blocks] matrix."""
+    u8 = _torch.uint8
+    if codes.dtype is not u8 or scales.dtype is not u8:
+        raise ValueError(f"{names[0]} and {names[1]} must be uint8, got {codes.dtype} and {scales.dtype}")
+    cs = _lm_rows(codes, rows, 16 * blocks, device, names[0])
+    ss = _lm_rows(scales, rows, blocks, device, names[1])
+    if rows <= 1 or blocks == 0:  # such a stride is free in torch, and the library takes whole blocks
+        cs = 16 * blocks
+    return codes.data_ptr(), cs, scales.data_ptr(), ss
+
+
+def _mx4_conversion(x, codes, scales):
+    device = _lm_device(x, "x")
+    code = _float_code(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, cols], got {list(x.shape)}")
+    rows, cols = x.size(0), x.size(1)
+    return device, code, rows, cols, _lm_rows(x, rows, cols, device, "x"), \
+        _mx4_matrix(codes, scales, rows, -(-cols // ZS_MX4_BLOCK), device, ("codes", "scales"))
+
+
+def zs_mx4_quantize(x, codes, scales, stream=None):
+    """Codes (uint8 [rows, 16 * blocks], two elements a byte) and scales (uint8 [rows, blocks]) of x, bfloat16 or
+    float32 [rows, cols], in blocks = ceil(cols / 32) blocks a row."""
+    device, code, rows, cols, xs, q = _mx4_conversion(x, codes, scales)
+    _lm_call(_lib.zs_mx4_quantize, device, stream, x.data_ptr(), code, rows, cols, xs, *q)
+
+
+def zs_mx4_dequantize(codes, scales, x, stream=None):
+    """x (bfloat16 or float32 [rows, cols]) from its codes and scales."""
+    device, code, rows, cols, xs, q = _mx4_conversion(x, codes, scales)
+    _lm_call(_lib.zs_mx4_dequantize, device, stream, *q, rows, cols, x.data_ptr(), code, xs)
+
+
+def zs_mx4_matmul(x_codes, x_scales, w_codes, w_scales, y, stream=None):
+    """y = X W^T (bfloat16 or float32 [rows, out_features]) of two quantized matrices: codes uint8 [rows, 16 * blocks]
+    and [out_features, 16 * blocks], scales uint8 [rows, blocks] and [out_features, blocks]."""
+    device = _lm_device(x_codes, "x_codes")
+    if x_scales.dim() != 2 or w_scales.dim() != 2:
+        raise ValueError(f"x_scales and w_scales must be matrices, got {list(x_scales.shape)} and "
+                         f"{list(w_scales.shape)}")
+    rows, blocks, out = x_scales.size(0), x_scales.size(1), w_scales.size(0)
+    x = _mx4_matrix(x_codes, x_scales, rows, blocks, device, ("x_codes", "x_scales"))
+    w = _mx4_matrix(w_codes, w_scales, out, blocks, device, ("w_codes", "w_scales"))
+    code = _float_code(y, "y")
+    _lm_call(_lib.zs_mx4_matmul, device, stream, *x, rows, *w, out, ZS_MX4_BLOCK * blocks, y.data_ptr(), code,
+             _lm_rows(y, rows, out, device, "y"))
+
+
+# ---------------------------------------------------------------- verification of drafted tokens
+
+
+def zs_verify_drafts_workspace_bytes(requests, drafts, vocab):
+    n = _lib.zs_verify_drafts_workspace_bytes(requests, drafts, vocab)
+    if n < 0:
+        raise ZsError(ZS_EINVAL, zs_last_error())
+    return n
+
+
+def zs_verify_drafts(target_logits, draft_tokens, uniforms, accepted, tokens, workspace, draft_logits=None,
+                     draft_lens=None, logprobs=None, temperature=1.0, stream=None):
+    """How many drafted tokens of each request stand, and the token drawn behind them. target_logits: bfloat16 or
+    float32 [requests * (drafts + 1), vocab]; draft_tokens: int32 [requests, drafts]; uniforms: float32
+    [requests, drafts + 1]; draft_logits (None: the drafted token was certain): like target_logits
+    [requests * drafts, vocab]; draft_lens (None: all have `drafts`): int32 [requests]. Outputs: accepted int32
+    [requests], tokens int32 and logprobs (optional) float32 [requests, drafts + 1]. workspace: uint8, of
+    zs_verify_drafts_workspace_bytes."""
+    device, code, places, vocab, stride = _lm_logits(target_logits)
+    if draft_tokens.dim() != 2:
+        raise ValueError(f"draft_tokens must be [requests, drafts], got {list(draft_tokens.shape)}")
+    requests, drafts = draft_tokens.size(0), draft_tokens.size(1)
+    if places != requests * (drafts + 1):
+        raise ValueError(f"target_logits must have {requests * (drafts + 1)} rows, got {places}")
+    i32, f32 = _torch.int32, _torch.float32
+    dp, ds = None, vocab
+    if draft_logits is not None:
+        if draft_logits.dtype is not target_logits.dtype:
+            raise ValueError(f"draft_logits must be {target_logits.dtype} like the target's, got {draft_logits.dtype}")
+        dp, ds = draft_logits.data_ptr(), _lm_rows(draft_logits, requests * drafts, vocab, device, "draft_logits")
+    _lm_call(_lib.zs_verify_drafts, device, stream, target_logits.data_ptr(), code, requests, drafts, vocab, stride,
+             dp, ds, _lm_array(draft_tokens, i32, requests * drafts, drafts, device, "draft_tokens") if drafts else None,
+             _lm_array(draft_lens, i32, requests, 0, device, "draft_lens"),
+             _lm_array(uniforms, f32, places, drafts + 1, device, "uniforms"), temperature,
+             _lm_array(accepted, i32, requests, 0, device, "accepted"),
+             _lm_array(tokens, i32, places, drafts + 1, device, "tokens"),
+             _lm_array(logprobs, f32, places, drafts + 1, device, "logprobs"),
+             _lm_flat(workspace, (_torch.uint8,), 0, device, "workspace"), workspace.numel())
 
 
 def zs_last_error():

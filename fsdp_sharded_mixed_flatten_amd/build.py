@@ -39,7 +39,7 @@ def build(verbose=False, out=None):
     """Builds libzs.so (or ``out``)."""
     os.makedirs(BUILD, exist_ok=True)
     objs = []
-    for name in ("zs_api", "zs_lm_api"):
+    for name in ("zs_api", "zs_lm_api", "zs_mx4_api", "zs_drafts_api", "zs_clip_api"):
         o = os.path.join(BUILD, f"{name}.o")
         _run(["g++", *COMMON, "-c", os.path.join(CSRC, f"{name}.cpp"), "-o", o], verbose)
         objs.append(o)
@@ -49,7 +49,7 @@ def build(verbose=False, out=None):
     _run(["g++", *COMMON, "-fno-math-errno", "-pthread", "-c", os.path.join(CSRC, "zs_host_adamw.cpp"), "-o",
           host_o], verbose)
     objs.append(host_o)
-    for name in ("zs_kernels", "zs_offload", "zs_matvec", "zs_loss"):
+    for name in ("zs_kernels", "zs_offload", "zs_matvec", "zs_loss", "zs_mx4", "zs_mx4_matmul", "zs_drafts", "zs_clip"):
         o = os.path.join(BUILD, f"{name}.o")
         _run([HIPCC, *COMMON, *HIP_ONLY, "-c", os.path.join(CSRC, f"{name}.hip"), "-o", o], verbose)
         objs.append(o)

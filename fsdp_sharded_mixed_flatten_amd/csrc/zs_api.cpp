@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "zs_internal.h"
+#include "zs_clip_internal.h"
 #include "zs_lm_internal.h"
 
 namespace {
@@ -821,8 +822,17 @@ zs_status zs_adamw_shard_step_accum_dc(const zs_plan* plan, const zs_adamw_coefs
 namespace {
 
 struct MultiLayout {
-    int64_t pieces_off, contribs_off, chunks_off, total;
+    int64_t pieces_off, contribs_off, chunks_off, unsummed_off, total;
 };
+
+// Whether some piece's squares are another rank's to count: replicated tensors
+// are rank 0's.
+bool has_unsummed(const zs_plan* p) {
+    if (p->rank == 0) return false;
+    for (const auto& t : p->tensors)
+        if (t.replicated) return true;
+    return false;
+}
 
 MultiLayout multi_layout(const zs_plan* p, int32_t n_contribs) {
     auto al = [](int64_t x) { return roundup(x, 256); };
@@ -831,7 +841,9 @@ MultiLayout multi_layout(const zs_plan* p, int32_t n_contribs) {
     L.pieces_off = al((int64_t)sizeof(zs::MultiHeader));
     L.contribs_off = al(L.pieces_off + n * (int64_t)sizeof(zs::PieceDev));
     L.chunks_off = al(L.contribs_off + n * (int64_t)n_contribs * (int64_t)sizeof(void*));
-    L.total = al(L.chunks_off + (int64_t)p->chunk_piece.size() * (int64_t)sizeof(int32_t));
+    const int64_t end = al(L.chunks_off + (int64_t)p->chunk_piece.size() * (int64_t)sizeof(int32_t));
+    L.unsummed_off = has_unsummed(p) ? end : 0;
+    L.total = L.unsummed_off ? al(end + n) : end;
     return L;
 }
 
@@ -969,6 +981,9 @@ zs_status zs_multi_bind(const zs_plan* plan, const zs_piece_ptrs* pieces, const 
         for (int32_t q = 0; q < n_contribs; ++q) cd[(int64_t)i * n_contribs + q] = contribs[(int64_t)q * n + i];
     }
     std::memcpy(host.data() + L.chunks_off, plan->chunk_piece.data(), plan->chunk_piece.size() * sizeof(int32_t));
+    if (L.unsummed_off)
+        for (int32_t i = 0; i < n; ++i)
+            host[(size_t)(L.unsummed_off + i)] = (char)plan->tensors[(size_t)i].replicated;
     trace("zs_multi_bind", plan, n_contribs, 0, plan->S, stream);
     if (zs_status st = hip_status(zs::copy_h2d_sync(workspace, host.data(), L.total, stream), "workspace copy"))
         return st;
@@ -1089,3 +1104,21 @@ zs_status zs_fused_shard_step_multi_groups(const zs_plan* plan, const zs_adamw_h
 }
 
 }  // extern "C"
+
+// For the clipping of the multi-tensor step (zs_clip_internal.h).
+namespace zs {
+
+zs_status bound_tables(const zs_plan* plan, const void* workspace, int32_t need, BoundTables* out) {
+    if (zs_status st = check_multi_plan(plan)) return st;
+    Binding b;
+    if (zs_status st = lookup_binding(plan, workspace, need, &b)) return st;
+    out->off = multi_offsets(plan, b.n_contribs);
+    out->unsummed = multi_layout(plan, b.n_contribs).unsummed_off;
+    return ZS_OK;
+}
+
+zs_status group_coefs(const zs_plan* plan, const zs_adamw_hparams* hps, int32_t n_groups, CoefTable* ct) {
+    return group_table(plan, hps, n_groups, ct);
+}
+
+}  // namespace zs

@@ -1,0 +1,244 @@
+// Clipping of the multi-tensor step for CDNA4 (gfx950): the squared norm of the
+// bf16 gradient over all bound pieces, and AdamW from the clipped gradient.
+//
+// Both are HBM streams over the chunks of the binding's table: 2 bytes an
+// element for the norm, 28 to 32 for the step.
+#include <hip/hip_runtime.h>
+
+#include "zs_clip_internal.h"
+
+namespace zs {
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Pointers read from a device table are generic to the compiler, which would
+// emit flat accesses for them; every buffer here is global memory.
+template <typename T>
+using gptr = __attribute__((address_space(1))) T*;
+template <typename T>
+__device__ __forceinline__ T ld_nt(const T* p) {
+    return __builtin_nontemporal_load((gptr<const T>)p);
+}
+template <typename T>
+__device__ __forceinline__ T ld_g(const T* p) {
+    return *(gptr<const T>)p;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// ------------------------------------------------------------------ the norm
+
+constexpr int kNormThreads = 256;
+constexpr int kLanesPerChunk = kChunkElems / 8;  // 16-byte loads
+constexpr int kRowChunks = kNormThreads / kLanesPerChunk;
+constexpr int kNormRows = (int)kNormChunks / kRowChunks;
+static_assert(kNormThreads % kLanesPerChunk == 0 && kNormChunks % kRowChunks == 0, "rows of whole chunks");
+
+__device__ __forceinline__ double squares(const u32x4& v, double s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double a = (double)lo_bf16(v[i]), b = (double)hi_bf16(v[i]);
+        s = fma(a, a, s);
+        s = fma(b, b, s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+
+// Sum and flag of a workgroup of WAVES waves, in thread 0.
+template <int WAVES>
+__device__ __forceinline__ void group_sum(double& s, bool& bad) {
+    __shared__ double sums[WAVES];
+    __shared__ int bads[WAVES];
+    s = wave_sum(s);
+    const bool any = __ballot(bad) != 0;
+    if ((threadIdx.x & 63) == 0) {
+        sums[threadIdx.x >> 6] = s;
+        bads[threadIdx.x >> 6] = any;
+    }
+    __syncthreads();
+    s = 0.0;
+    bad = false;
+    for (int i = 0; i < WAVES; ++i) {
+        s += sums[i];
+        bad |= bads[i] != 0;
+    }
+}
+
+// Workgroup g adds up chunks [g * kNormChunks, (g + 1) * kNormChunks). A square
+// of a bf16 is finite in double, and so is any sum of them: a sum that is not
+// comes from an element that is not.
+__global__ __launch_bounds__(kNormThreads) void k_multi_norm(const MultiHeader* __restrict__ hdr, MultiOffsets moff,
+                                                             int64_t unsummed, int64_t n_chunks,
+                                                             double* __restrict__ part, int32_t* __restrict__ flags) {
+    const char* ws = reinterpret_cast<const char*>(hdr);
+    const int32_t* cpiece = reinterpret_cast<const int32_t*>(ws + moff.chunks);
+    const PieceDev* pieces = reinterpret_cast<const PieceDev*>(ws + moff.pieces);
+    const uint8_t* skip = unsummed ? reinterpret_cast<const uint8_t*>(ws + unsummed) : nullptr;
+    double s = 0.0;
+    bool bad = false;
+    if (hdr->magic == kMultiMagic) {  // else not a bound table: nothing of it is followed
+        const int64_t c0 = (int64_t)blockIdx.x * kNormChunks;
+        const int off = (threadIdx.x % kLanesPerChunk) * 8;
+        int32_t chunk[kNormRows], piece[kNormRows];
+        bool ok[kNormRows];
+#pragma unroll
+        for (int r = 0; r < kNormRows; ++r) {
+            const int64_t c = c0 + r * kRowChunks + threadIdx.x / kLanesPerChunk;
+            ok[r] = c < n_chunks;
+            chunk[r] = ok[r] ? (int32_t)c : 0;
+            piece[r] = ld_g(cpiece + chunk[r]);
+        }
+        u32x4 v[kNormRows];
+        bool counts[kNormRows];
+#pragma unroll
+        for (int r = 0; r < kNormRows; ++r) {
+            const PieceDev* pc = pieces + piece[r];
+            const int64_t at = (int64_t)(chunk[r] - ld_g(&pc->first_chunk)) * kChunkElems + off;
+            ok[r] = ok[r] && at < ld_g(&pc->len);  // lengths are multiples of 8
+            counts[r] = !skip || !ld_g(skip + piece[r]);
+            v[r] = u32x4{0, 0, 0, 0};
+            if (ok[r]) v[r] = ld_nt(reinterpret_cast<const u32x4*>(static_cast<const char*>(ld_g(&pc->grad)) + 2 * at));
+        }
+#pragma unroll
+        for (int r = 0; r < kNormRows; ++r) {
+            const double t = squares(v[r], 0.0);
+            bad |= !__builtin_isfinite(t);
+            if (counts[r]) s += t;
+        }
+    }
+    group_sum<kNormThreads / 64>(s, bad);
+    if (threadIdx.x == 0) {
+        part[blockIdx.x] = s;
+        flags[blockIdx.x] = bad;
+    }
+}
+
+// One workgroup: thread i adds up sums i, i + 1024, ... in order.
+constexpr int kFinalThreads = 1024;
+__global__ __launch_bounds__(kFinalThreads) void k_multi_norm_final(const double* __restrict__ part,
+                                                                    const int32_t* __restrict__ flags, int64_t n,
+                                                                    double* __restrict__ sumsq_out,
+                                                                    int32_t* __restrict__ nonfinite_out) {
+    double s = 0.0;
+    bool bad = false;
+    for (int64_t i = threadIdx.x; i < n; i += kFinalThreads) {
+        s += part[i];
+        bad |= flags[i] != 0;
+    }
+    group_sum<kFinalThreads / 64>(s, bad);
+    if (threadIdx.x == 0) {
+        *sumsq_out = s;
+        *nonfinite_out = bad ? 1 : 0;
+    }
+}
+
+// ------------------------------------------------------------------ the step
+
+// Round to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+    const uint32_t u = __float_as_uint(f);
+    const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+    return ((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r;
+}
+
+// The element arithmetic of zs_adamw_shard_step, operation by operation in its
+// order (fp32, one rounding each): the two steps give the same bits where the
+// factor is 1.
+__device__ __forceinline__ void adamw(const AdamCoef& c, float g, float& w, float& m, float& v) {
+    const float wd = w * c.decay;
+    m = c.b1 * m + c.omb1 * g;
+    v = c.b2 * v + c.omb2 * (g * g);
+    w = wd - c.lr * ((m / c.bc1) / (sqrtf(v / c.bc2) + c.eps));
+}
+
+// Stores of a row that the whole wave writes: a buffer resource at the row's
+// first unit, whose access carries the nontemporal policy with sc1, which a
+// global store cannot (3-4% faster than nontemporal alone in the unclipped step).
+constexpr int kBufferWord3 = 0x00020000, kStreamAux = 2 | 16;
+template <typename T>
+__device__ __forceinline__ void st_lane(T* p, T x) {
+    const uintptr_t row = reinterpret_cast<uintptr_t>(p - threadIdx.x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)row);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(row >> 32));
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>(((uintptr_t)hi << 32) | lo), (short)0, kBlockThreads * (int)sizeof(T), kBufferWord3);
+    const int off = (int)(threadIdx.x * sizeof(T));
+    if constexpr (sizeof(T) == 16)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, kStreamAux);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, off, 0, kStreamAux);
+}
+
+// One chunk (four elements a lane) a workgroup of one wave, as the unclipped
+// multi-tensor step.
+constexpr unsigned kStepLds = 12u << 10;  // unused: fewer waves a compute unit keep fewer DRAM rows in play
+__global__ __launch_bounds__(kBlockThreads) void k_multi_clip(CoefTable ct, const MultiHeader* __restrict__ hdr,
+                                                              MultiOffsets off, const float* __restrict__ scale_p,
+                                                              const int32_t* __restrict__ skip_p) {
+    if (hdr->magic != kMultiMagic) return;
+    if (skip_p && *skip_p) return;  // uniform: the whole grid skips the step
+    const float scale = scale_p ? *scale_p : 1.0f;
+    const char* ws = reinterpret_cast<const char*>(hdr);
+    const int32_t piece = reinterpret_cast<const int32_t*>(ws + off.chunks)[blockIdx.x];
+    const PieceDev pc = reinterpret_cast<const PieceDev*>(ws + off.pieces)[piece];
+    const AdamCoef c = ct.c[pc.group];
+    const int64_t start = (int64_t)((int32_t)blockIdx.x - pc.first_chunk) * kChunkElems;
+    const int64_t u = (start >> 2) + threadIdx.x;
+    if (u >= pc.len >> 2) return;
+    const u32x2 g = ld_nt(reinterpret_cast<const u32x2*>(pc.grad) + u);
+    f32x4 w = ld_nt(reinterpret_cast<const f32x4*>(pc.master) + u);
+    f32x4 m = ld_nt(reinterpret_cast<const f32x4*>(pc.m) + u);
+    f32x4 v = ld_nt(reinterpret_cast<const f32x4*>(pc.v) + u);
+    const float ge[4] = {lo_bf16(g.x), hi_bf16(g.x), lo_bf16(g.y), hi_bf16(g.y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float we = w[e], me = m[e], ve = v[e];
+        adamw(c, ge[e] * scale, we, me, ve);
+        w[e] = we;
+        m[e] = me;
+        v[e] = ve;
+    }
+    st_lane(reinterpret_cast<f32x4*>(pc.master) + u, w);
+    st_lane(reinterpret_cast<f32x4*>(pc.m) + u, m);
+    st_lane(reinterpret_cast<f32x4*>(pc.v) + u, v);
+    const u32x2 p{bf16_rne(w[0]) | (bf16_rne(w[1]) << 16), bf16_rne(w[2]) | (bf16_rne(w[3]) << 16)};
+    if (hdr->flags & kHasParam) st_lane(reinterpret_cast<u32x2*>(pc.param) + u, p);
+    if (hdr->flags & kHasFull) st_lane(reinterpret_cast<u32x2*>(pc.full_own) + u, p);
+}
+
+}  // namespace
+
+int launch_multi_norm(const void* workspace, const BoundTables& t, int64_t n_chunks, double* sumsq_out,
+                      int32_t* nonfinite_out, void* stats_workspace, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t n = norm_groups(n_chunks);
+    double* part = static_cast<double*>(stats_workspace);
+    int32_t* flags = reinterpret_cast<int32_t*>(part + n);
+    if (n > 0) {
+        k_multi_norm<<<(unsigned)n, kNormThreads, 0, s>>>(static_cast<const MultiHeader*>(workspace), t.off,
+                                                          t.unsummed, n_chunks, part, flags);
+        if (hipError_t e = hipGetLastError()) return (int)e;
+    }
+    k_multi_norm_final<<<1, kFinalThreads, 0, s>>>(part, flags, n, sumsq_out, nonfinite_out);
+    return (int)hipGetLastError();
+}
+
+int launch_multi_clip(const CoefTable& c, const void* workspace, const BoundTables& t, int64_t n_chunks,
+                      const float* scale, const int32_t* skip, void* stream) {
+    if (n_chunks == 0) return 0;
+    k_multi_clip<<<(unsigned)n_chunks, kBlockThreads, kStepLds, static_cast<hipStream_t>(stream)>>>(
+        c, static_cast<const MultiHeader*>(workspace), t.off, scale, skip);
+    return (int)hipGetLastError();
+}
+
+}  // namespace zs

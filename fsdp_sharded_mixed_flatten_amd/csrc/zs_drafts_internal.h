@@ -1,0 +1,61 @@
+// Kernel launcher of the verification of drafted tokens (zs_drafts.h) and its
+// workspace. Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "../../include/zs_drafts.h"
+#include "zs_lm_internal.h"
+
+namespace zs {
+
+// Logits of a row that one workgroup sums.
+constexpr int64_t kVerifyChunk = 8192;
+
+// Largest logit of a chunk and the sum of its exponentials relative to that
+// logit, in 64 bits. A NaN or +infinity in the chunk: top is NaN.
+struct VerifyPart {
+    double top, sum;
+};
+
+// What the first workgroup of a request leaves for the draw.
+struct VerifyPick {
+    double p_top, p_sum, q_top, q_sum;
+    int32_t at;     // the place the token is drawn for
+    int32_t kind;   // VerifyKind
+    int32_t token;  // the drafted token that fell
+    int32_t unused;
+};
+enum VerifyKind : int32_t { kDrawNothing = 0, kDrawTarget = 1, kDrawRest = 2 };
+
+// The workspace: parts [rows, chunks], the target's rows before the drafts';
+// totals [requests, chunks]; picks [requests].
+struct VerifyLayout {
+    int64_t chunks, rows, totals_off, picks_off, bytes;
+};
+inline VerifyLayout verify_layout(int64_t requests, int32_t drafts, int64_t vocab) {
+    VerifyLayout l;
+    l.chunks = (vocab + kVerifyChunk - 1) / kVerifyChunk;
+    l.rows = requests * (2 * (int64_t)drafts + 1);
+    l.totals_off = l.rows * l.chunks * (int64_t)sizeof(VerifyPart);
+    l.picks_off = l.totals_off + (requests * l.chunks * 8 + 15) / 16 * 16;
+    l.bytes = l.picks_off + requests * (int64_t)sizeof(VerifyPick);
+    return l;
+}
+
+struct VerifyArgs {
+    Rows target, draft;  // draft.p may be NULL
+    int64_t requests, vocab;
+    int32_t drafts;
+    const int32_t* tokens;
+    const int32_t* lens;  // may be NULL
+    const float* uniforms;
+    int32_t* accepted;
+    int32_t* out;
+    float* logprobs;  // may be NULL
+};
+
+// Returns a hipError_t value cast to int.
+int launch_verify(const VerifyArgs& a, int dtype, double temperature, void* workspace, void* stream);
+
+}  // namespace zs
