@@ -88,32 +88,61 @@ __global__ __launch_bounds__(kNormThreads) void k_multi_norm(const MultiHeader* 
     bool bad = false;
     if (hdr->magic == kMultiMagic) {  // else not a bound table: nothing of it is followed
         const int64_t c0 = (int64_t)blockIdx.x * kNormChunks;
-        const int off = (threadIdx.x % kLanesPerChunk) * 8;
-        int32_t chunk[kNormRows], piece[kNormRows];
-        bool ok[kNormRows];
-#pragma unroll
-        for (int r = 0; r < kNormRows; ++r) {
-            const int64_t c = c0 + r * kRowChunks + threadIdx.x / kLanesPerChunk;
-            ok[r] = c < n_chunks;
-            chunk[r] = ok[r] ? (int32_t)c : 0;
-            piece[r] = ld_g(cpiece + chunk[r]);
-        }
+        const int64_t c1 = c0 + kNormChunks < n_chunks ? c0 + kNormChunks : n_chunks;
+        const int32_t first = cpiece[c0], last = cpiece[c1 - 1];
         u32x4 v[kNormRows];
-        bool counts[kNormRows];
+        if (first == last) {  // chunks follow their pieces' order: the whole range is of one
+            const PieceDev pc = pieces[first];
+            const int64_t at = (c0 - pc.first_chunk) * kChunkElems, end = (c1 - pc.first_chunk) * kChunkElems;
+            const char* g = static_cast<const char*>(pc.grad) + 2 * at;
+            const int n = (int)((end < pc.len ? end : pc.len) - at) / 8;  // lengths are multiples of 8
+            if (n == kNormRows * kNormThreads) {
 #pragma unroll
-        for (int r = 0; r < kNormRows; ++r) {
-            const PieceDev* pc = pieces + piece[r];
-            const int64_t at = (int64_t)(chunk[r] - ld_g(&pc->first_chunk)) * kChunkElems + off;
-            ok[r] = ok[r] && at < ld_g(&pc->len);  // lengths are multiples of 8
-            counts[r] = !skip || !ld_g(skip + piece[r]);
-            v[r] = u32x4{0, 0, 0, 0};
-            if (ok[r]) v[r] = ld_nt(reinterpret_cast<const u32x4*>(static_cast<const char*>(ld_g(&pc->grad)) + 2 * at));
-        }
+                for (int r = 0; r < kNormRows; ++r)
+                    v[r] = ld_nt(reinterpret_cast<const u32x4*>(g) + r * kNormThreads + threadIdx.x);
+            } else {
 #pragma unroll
-        for (int r = 0; r < kNormRows; ++r) {
-            const double t = squares(v[r], 0.0);
-            bad |= !__builtin_isfinite(t);
-            if (counts[r]) s += t;
+                for (int r = 0; r < kNormRows; ++r) {
+                    const int i = r * kNormThreads + threadIdx.x;
+                    v[r] = ld_nt(reinterpret_cast<const u32x4*>(g) + (i < n ? i : 0));
+                    if (i >= n) v[r] = u32x4{0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kNormRows; ++r) s = squares(v[r], s);
+            bad = !__builtin_isfinite(s);
+            if (skip && skip[first]) s = 0.0;
+        } else {
+            // every row's lookups, then every row's load, without a branch
+            // between: a lane past its chunk's end reads the chunk's first vector
+            int32_t chunk[kNormRows], piece[kNormRows];
+            bool ok[kNormRows], counts[kNormRows];
+            const u32x4* from[kNormRows];
+            const int off = (threadIdx.x % kLanesPerChunk) * 8;
+#pragma unroll
+            for (int r = 0; r < kNormRows; ++r) {
+                const int64_t c = c0 + r * kRowChunks + threadIdx.x / kLanesPerChunk;
+                ok[r] = c < c1;
+                chunk[r] = (int32_t)(ok[r] ? c : c0);
+                piece[r] = ld_g(cpiece + chunk[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < kNormRows; ++r) {
+                const PieceDev* pc = pieces + piece[r];
+                const int64_t at = (int64_t)(chunk[r] - ld_g(&pc->first_chunk)) * kChunkElems;
+                ok[r] = ok[r] && at + off < ld_g(&pc->len);
+                counts[r] = !skip || !ld_g(skip + piece[r]);
+                from[r] = reinterpret_cast<const u32x4*>(static_cast<const char*>(ld_g(&pc->grad)) +
+                                                         2 * (at + (ok[r] ? off : 0)));
+            }
+#pragma unroll
+            for (int r = 0; r < kNormRows; ++r) v[r] = ld_nt(from[r]);
+#pragma unroll
+            for (int r = 0; r < kNormRows; ++r) {
+                const double t = ok[r] ? squares(v[r], 0.0) : 0.0;
+                bad |= !__builtin_isfinite(t);
+                if (counts[r]) s += t;
+            }
         }
     }
     group_sum<kNormThreads / 64>(s, bad);
