@@ -109,12 +109,201 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4 x, int64_t rows,
     }
 }
 
+// ------------------------------------------------------------------ many rows
+// A workgroup computes a tile of BM rows of x by BN of W, its WM x WN waves
+// 32 TM x 32 TN each. Both sides' codes go through shared memory, 256 columns
+// at a time, straight from global memory: the next 256 are on their way while
+// the present ones are multiplied. A row's 128 bytes are eight 16-byte blocks,
+// and block c of row r lies at place c ^ (r % 8), so that lanes that read one
+// block of many rows spread over the banks.
+// A lane of a 32 x 32 instruction gives block l / 32 of row l % 32. Which 64
+// columns an instruction takes is free as long as both sides agree: the lower
+// lanes take blocks 0 to 3 of the eight in their four turns and the upper ones 4
+// to 7, so that a lane's four scales are one word, whose bytes the
+// instruction's operand selection picks.
+template <int TM_, int TN_, int WM_, int WN_>
+struct Tile {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+    static constexpr int kThreads = 64 * WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
+    static constexpr int kUnits = (BM + BN) * 8 / kThreads;  // 16-byte loads of a thread a turn
+    static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && kThreads % 64 == 0, "whole loads");
+};
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int STEP>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& x, uint32_t sx, const u32x4& w, uint32_t sw, f32x16 acc) {
+    const i32x8 a{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    const i32x8 b{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFp4, kFp4, STEP, (int)sx, STEP, (int)sw);
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+template <typename T>
+struct Shared {
+    u32x4 codes[2][(T::BM + T::BN) * 8];
+    uint32_t scales[2][4][T::BM + T::BN];
+};
+
+template <typename T, int STEP>
+__device__ __forceinline__ void turn_step(const u32x4* x, const u32x4* w, const uint32_t* sx, const uint32_t* sw,
+                                          int half, f32x16 (&acc)[T::TM][T::TN]) {
+    const int r = threadIdx.x & 31, place = (4 * half + STEP) ^ (r & 7);
+    u32x4 a[T::TM], b[T::TN];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) a[i] = x[(32 * i + r) * 8 + place];
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) b[j] = w[(32 * j + r) * 8 + place];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) acc[i][j] = mfma32<STEP>(a[i], sx[i], b[j], sw[j], acc[i][j]);
+}
+
+// A pointer that is the same in every lane, in scalar registers.
+__device__ __forceinline__ char* uniform(const void* p) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    return reinterpret_cast<char*>(((uintptr_t)hi << 32) | lo);
+}
+
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void k_mx4_tiled(Mx4 x, int rows, Mx4 w, int out, int blocks,
+                                                           void* __restrict__ y, int y_bf16, int64_t y_stride,
+                                                           int tiles_m) {
+    __shared__ Shared<T> sh;
+    const int tid = threadIdx.x, half = (tid & 63) >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tile = blockIdx.x;
+    const int r0 = tile % tiles_m * T::BM, o0 = tile / tiles_m * T::BN;
+    const int mine_x = min(rows - r0, T::BM), mine_w = min(out - o0, T::BN);
+    const int xs = (int)x.code_stride, ws = (int)w.code_stride;
+    // what a load leaves out (rows past the end, blocks past the last) is asked
+    // for behind the buffer's end, where a load gives 0
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride), (short)0, (mine_x - 1) * xs + blocks * 16,
+        0x00020000);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        uniform(static_cast<const char*>(w.codes) + o0 * w.code_stride), (short)0, (mine_w - 1) * ws + blocks * 16,
+        0x00020000);
+    constexpr int kNowhere = 0x7FFFFFF0;
+    const int lrow = tid >> 3, lblock = (tid & 7) ^ (lrow & 7);
+    auto fetch = [&](int turn, int stage) {
+        const bool in = turn * 8 + lblock < blocks;
+        const int col = (turn * 8 + lblock) * 16;
+#pragma unroll
+        for (int u = 0; u < T::BM * 8 / T::kThreads; ++u) {
+            const int row = u * (T::kThreads / 8) + lrow;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64], 16,
+                                                     in && row < mine_x ? row * xs + col : kNowhere, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < T::BN * 8 / T::kThreads; ++u) {
+            const int row = u * (T::kThreads / 8) + lrow;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                wr, (lds_ptr)&sh.codes[stage][T::BM * 8 + u * T::kThreads + wave * 64], 16,
+                in && row < mine_w ? row * ws + col : kNowhere, 0, 0, 0);
+        }
+    };
+    // scales of 512 columns of a row: 16 bytes, through registers
+    constexpr int kScaleRows = (T::BM + T::BN) / T::kThreads;
+    static_assert(kScaleRows * T::kThreads == T::BM + T::BN, "a thread fetches the scales of whole rows");
+    u32x4 held[kScaleRows];
+    const uint8_t* sp[kScaleRows];
+#pragma unroll
+    for (int k = 0; k < kScaleRows; ++k) {
+        const int row = k * T::kThreads + tid;
+        sp[k] = row < T::BM ? static_cast<const uint8_t*>(x.scales) + (r0 + min(row, mine_x - 1)) * x.scale_stride
+                            : static_cast<const uint8_t*>(w.scales) + (o0 + min(row - T::BM, mine_w - 1)) * w.scale_stride;
+    }
+    auto fetch_scales = [&](int pair) {
+        if ((pair + 1) * 16 <= blocks) {
+#pragma unroll
+            for (int k = 0; k < kScaleRows; ++k) held[k] = *reinterpret_cast<const u32x4_u1*>(sp[k] + pair * 16);
+        } else {  // the last, byte by byte; nothing reads this half of sh.scales now
+#pragma unroll
+            for (int k = 0; k < kScaleRows; ++k) {
+                uint8_t* to = reinterpret_cast<uint8_t*>(&sh.scales[pair & 1][0][k * T::kThreads + tid]);
+                uint8_t b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) b[i] = sp[k][min(pair * 16 + i, blocks - 1)];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    to[i / 4 * 4 * (T::BM + T::BN) + i % 4] = pair * 16 + i < blocks ? b[i] : (uint8_t)127;
+            }
+        }
+    };
+    auto put_scales = [&](int pair) {
+        if ((pair + 1) * 16 <= blocks) {
+#pragma unroll
+            for (int k = 0; k < kScaleRows; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sh.scales[pair & 1][i][k * T::kThreads + tid] = held[k][i];
+        }
+    };
+    f32x16 acc[T::TM][T::TN];
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) acc[i][j] = f32x16{};
+    const int wm = wave % T::WM, wn = wave / T::WM;
+    const int turns = (blocks + 7) / 8;
+    fetch(0, 0);
+    fetch_scales(0);
+    put_scales(0);
+    for (int t = 0; t < turns; ++t) {
+        __syncthreads();  // turn t's codes and scales are there, turn t - 1's no longer read
+        const int stage = t & 1, pair = t >> 1;
+        if (t + 1 < turns) fetch(t + 1, stage ^ 1);
+        if (stage == 0 && t + 2 < turns) fetch_scales(pair + 1);
+        uint32_t sx[T::TM], sw[T::TN];
+        const uint32_t* plane = sh.scales[pair & 1][2 * stage + half];
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) sx[i] = plane[32 * (wm * T::TM + i) + (tid & 31)];
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) sw[j] = plane[T::BM + 32 * (wn * T::TN + j) + (tid & 31)];
+        const u32x4* xt = sh.codes[stage] + 32 * wm * T::TM * 8;
+        const u32x4* wt = sh.codes[stage] + (T::BM + 32 * wn * T::TN) * 8;
+        turn_step<T, 0>(xt, wt, sx, sw, half, acc);
+        turn_step<T, 1>(xt, wt, sx, sw, half, acc);
+        turn_step<T, 2>(xt, wt, sx, sw, half, acc);
+        turn_step<T, 3>(xt, wt, sx, sw, half, acc);
+        if (stage == 1 && t + 1 < turns) put_scales(pair + 1);
+    }
+    // lane l has column l % 32 and rows 8 * (e / 4) + 4 * (l / 32) + e % 4
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+            const int col = o0 + 32 * (wn * T::TN + j) + (tid & 31);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = r0 + 32 * (wm * T::TM + i) + 8 * (e / 4) + 4 * half + e % 4;
+                if (row < rows && col < out) store_y(y, y_bf16, row * y_stride + col, acc[i][j][e]);
+            }
+        }
+}
+
+template <typename T>
+int launch_tiled(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
+                 int64_t y_stride, hipStream_t s) {
+    const int64_t tm = (rows + T::BM - 1) / T::BM, tn = (out + T::BN - 1) / T::BN;
+    k_mx4_tiled<T><<<(unsigned)(tm * tn), T::kThreads, 0, s>>>(x, (int)rows, w, (int)out, (int)blocks, y, y_bf16, y_stride,
+                                                              (int)tm);
+    return (int)hipGetLastError();
+}
+
 }  // namespace
 
 int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_features, int64_t blocks, void* y,
                       int y_dtype, int64_t y_stride, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const int esz = y_dtype == ZS_DTYPE_BF16 ? 2 : 4;
+    if (rows > 64 && blocks > 0 && x.code_stride <= (1 << 22) && w.code_stride <= (1 << 22))
+        return launch_tiled<Tile<4, 4, 2, 2>>(x, rows, w, out_features, blocks, y, y_dtype == ZS_DTYPE_BF16, y_stride,
+                                              s);
     // a launch covers at most 2^32 - 1 work-items and 65535 tiles of rows
     const int64_t tiles = (out_features + 15) / 16;
     const int64_t fit = ((int64_t(1) << 32) - 1) / (tiles * 64 * kFewWaves);
