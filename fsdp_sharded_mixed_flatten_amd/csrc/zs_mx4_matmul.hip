@@ -33,6 +33,29 @@ __device__ __forceinline__ void store_y(void* y, bool bf16, int64_t i, float v) 
         static_cast<float*>(y)[i] = v;
 }
 
+// Four results side by side, `left` of which there are, k elements behind `at`.
+// The hardware's conversion rounds to nearest even but for one value in 2^17 next
+// to a tie, half a step and 2^-16 of one off.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_u2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_u4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ void store4(char* at, bool bf16, int k, const float (&v)[4], int left) {
+    if (left >= 4) {
+        if (bf16)
+            *reinterpret_cast<u32x2_u2*>(at + 2 * k) = u32x2_u2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        else
+            *reinterpret_cast<f32x4_u4*>(at + 4 * k) = f32x4_u4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < left) store_y(at, bf16, k + i, v[i]);
+    }
+}
+
 // 16 x 16 products of 128 columns. Lane l gives block l / 16 of row l % 16 of
 // either side and has rows 4 * (l / 16) .. + 3 of x and column l % 16 of y.
 __device__ __forceinline__ f32x4 mfma16(const u32x4& x, uint32_t sx, const u32x4& w, uint32_t sw, f32x4 acc) {
@@ -110,56 +133,43 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4 x, int64_t rows,
 }
 
 // ------------------------------------------------------------------ many rows
-// A workgroup computes a tile of BM rows of x by BN of W, its WM x WN waves
-// 32 TM x 32 TN each. Both sides' codes go through shared memory, 256 columns
-// at a time, straight from global memory: the next 256 are on their way while
-// the present ones are multiplied. A row's 128 bytes are eight 16-byte blocks,
-// and block c of row r lies at place c ^ (r % 8), so that lanes that read one
-// block of many rows spread over the banks.
-// A lane of a 32 x 32 instruction gives block l / 32 of row l % 32. Which 64
+// A workgroup computes BW columns of y (rows of W) for BX rows of x, its WW x WX
+// waves 32 TW x 32 TX each. Both sides' codes go straight from global to shared
+// memory, 128 columns (a turn) at a time through a ring of four stages: while
+// a turn is multiplied the next three are on their way or there. A row's 64
+// bytes are four 16-byte blocks; block c of row r lies at place c ^ (r / 4 % 4),
+// so that the sixteen lanes that are served together reach all banks.
+// A lane of a 32 x 32 instruction gives one block of row l % 32. Which 64
 // columns an instruction takes is free as long as both sides agree: the lower
-// lanes take blocks 0 to 3 of the eight in their four turns and the upper ones 4
-// to 7, so that a lane's four scales are one word, whose bytes the
-// instruction's operand selection picks.
-template <int TM_, int TN_, int WM_, int WN_>
+// lanes take blocks 0 and 1 of a turn's four, the upper ones 2 and 3, so that a
+// lane's two scales are neighbouring bytes, which the instruction's operand
+// selection picks. W gives the rows of an instruction's result, so that a lane
+// holds four columns of y side by side.
+template <int TW_, int TX_, int WW_, int WX_>
 struct Tile {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
-    static constexpr int kThreads = 64 * WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
-    static constexpr int kUnits = (BM + BN) * 8 / kThreads;  // 16-byte loads of a thread a turn
-    static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && kThreads % 64 == 0, "whole loads");
+    static constexpr int TW = TW_, TX = TX_, WW = WW_, WX = WX_;
+    static constexpr int kThreads = 64 * WW * WX, BW = 32 * TW * WW, BX = 32 * TX * WX, kRows = BW + BX;
+    static constexpr int kLoads = kRows * 4 / kThreads;  // 16-byte loads of a thread a turn
+    static constexpr int kScaleLoads = (kRows + kThreads - 1) / kThreads;
+    static_assert(BW * 4 % kThreads == 0 && BX * 4 % kThreads == 0, "whole loads");
 };
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int STEP>
-__device__ __forceinline__ f32x16 mfma32(const u32x4& x, uint32_t sx, const u32x4& w, uint32_t sw, f32x16 acc) {
-    const i32x8 a{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-    const i32x8 b{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFp4, kFp4, STEP, (int)sx, STEP, (int)sw);
+__device__ __forceinline__ f32x16 mfma32(const u32x4& w, uint32_t sw, const u32x4& x, uint32_t sx, f32x16 acc) {
+    const i32x8 a{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    const i32x8 b{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFp4, kFp4, STEP, (int)sw, STEP, (int)sx);
 }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 template <typename T>
 struct Shared {
-    u32x4 codes[2][(T::BM + T::BN) * 8];
-    uint32_t scales[2][4][T::BM + T::BN];
+    u32x4 codes[4][T::kRows * 4];
+    uint32_t scales[2][4][T::kRows];  // of 512 columns, two of them in turn: a word a turn and row
 };
-
-template <typename T, int STEP>
-__device__ __forceinline__ void turn_step(const u32x4* x, const u32x4* w, const uint32_t* sx, const uint32_t* sw,
-                                          int half, f32x16 (&acc)[T::TM][T::TN]) {
-    const int r = threadIdx.x & 31, place = (4 * half + STEP) ^ (r & 7);
-    u32x4 a[T::TM], b[T::TN];
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i) a[i] = x[(32 * i + r) * 8 + place];
-#pragma unroll
-    for (int j = 0; j < T::TN; ++j) b[j] = w[(32 * j + r) * 8 + place];
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) acc[i][j] = mfma32<STEP>(a[i], sx[i], b[j], sw[j], acc[i][j]);
-}
 
 // A pointer that is the same in every lane, in scalar registers.
 __device__ __forceinline__ char* uniform(const void* p) {
@@ -169,129 +179,200 @@ __device__ __forceinline__ char* uniform(const void* p) {
     return reinterpret_cast<char*>(((uintptr_t)hi << 32) | lo);
 }
 
+// One 64-column step's operands of a wave.
+template <typename T>
+struct Step {
+    u32x4 w[T::TW], x[T::TX];
+};
+template <typename T>
+struct Scales {
+    uint32_t w[T::TW], x[T::TX];
+};
+
+template <typename T>
+struct Tiled {
+    Shared<T>& sh;
+    __amdgpu_buffer_rsrc_t wr, xr;
+    int blocks;
+    int wave, lblock;           // the block of a turn that this thread's loads take
+    uint32_t from[T::kLoads];   // and where in W and x they find it in turn 0
+    int read_w, read_x;      // the row of a tile whose blocks this lane reads, times 4
+    int swizzle, half;
+    const uint8_t* scale_row[T::kScaleLoads];
+    u32x4 held[T::kScaleLoads];
+
+    // What a load leaves out (rows past the end, blocks past the last) is asked
+    // for behind the buffer's end, where a load gives 0. Buffers are shorter than
+    // 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
+    static constexpr uint32_t kNowhere = 0x7FFFFFF0u;
+    static constexpr int kLoadRows = T::kThreads / 4;
+    __device__ __forceinline__ void fetch(int turn, int stage) {
+        const uint32_t add = turn * 4 + lblock < blocks ? turn * 64u : kNowhere;
+#pragma unroll
+        for (int u = 0; u < T::kLoads; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(u < T::BW / kLoadRows ? wr : xr,
+                                                     (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64], 16,
+                                                     (int)(from[u] + add), 0, 0, 0);
+    }
+    // Scales of 512 columns (16 bytes a row) go through registers.
+    __device__ __forceinline__ void fetch_scales(int group) {
+        if ((group + 1) * 16 <= blocks) {
+#pragma unroll
+            for (int k = 0; k < T::kScaleLoads; ++k)
+                held[k] = *reinterpret_cast<const u32x4_u1*>(scale_row[k] + group * 16);
+        } else {  // the last: what lies behind the row's end is 1
+#pragma unroll
+            for (int k = 0; k < T::kScaleLoads; ++k) {
+                uint32_t b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) b[i] = scale_row[k][min(group * 16 + i, blocks - 1)];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) b[i] = group * 16 + i < blocks ? b[i] : 127;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    held[k][i] = b[4 * i] | (b[4 * i + 1] << 8) | (b[4 * i + 2] << 16) | (b[4 * i + 3] << 24);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_scales(int group) {
+#pragma unroll
+        for (int k = 0; k < T::kScaleLoads; ++k) {
+            const int row = k * T::kThreads + threadIdx.x;
+            if (T::kRows % T::kThreads == 0 || row < T::kRows)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sh.scales[group & 1][i][row] = held[k][i];
+        }
+    }
+    __device__ __forceinline__ void read(int stage, int step, Step<T>& f) const {
+        const int place = (2 * half + step) ^ swizzle;
+#pragma unroll
+        for (int i = 0; i < T::TW; ++i) f.w[i] = sh.codes[stage][read_w + 128 * i + place];
+#pragma unroll
+        for (int i = 0; i < T::TX; ++i) f.x[i] = sh.codes[stage][4 * T::BW + read_x + 128 * i + place];
+    }
+    __device__ __forceinline__ void read_scales(int group, int turn, Scales<T>& s) const {
+#pragma unroll
+        for (int i = 0; i < T::TW; ++i) s.w[i] = sh.scales[group & 1][turn][read_w / 4 + 32 * i] >> (16 * half);
+#pragma unroll
+        for (int i = 0; i < T::TX; ++i) s.x[i] = sh.scales[group & 1][turn][T::BW + read_x / 4 + 32 * i] >> (16 * half);
+    }
+    template <int STEP>
+    __device__ __forceinline__ void multiply(const Step<T>& f, const Scales<T>& s, f32x16 (&acc)[T::TW][T::TX]) const {
+#pragma unroll
+        for (int i = 0; i < T::TW; ++i)
+#pragma unroll
+            for (int j = 0; j < T::TX; ++j) acc[i][j] = mfma32<STEP>(f.w[i], s.w[i], f.x[j], s.x[j], acc[i][j]);
+    }
+};
+
+// All but the N youngest of this wave's loads are there, and all waves are here.
+// (A barrier of the language would wait for all loads.)
+template <int N>
+__device__ __forceinline__ void arrive() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void k_mx4_tiled(Mx4 x, int rows, Mx4 w, int out, int blocks,
                                                            void* __restrict__ y, int y_bf16, int64_t y_stride,
-                                                           int tiles_m) {
+                                                           int tiles_x) {
     __shared__ Shared<T> sh;
-    const int tid = threadIdx.x, half = (tid & 63) >> 5;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tile = blockIdx.x;
-    const int r0 = tile % tiles_m * T::BM, o0 = tile / tiles_m * T::BN;
-    const int mine_x = min(rows - r0, T::BM), mine_w = min(out - o0, T::BN);
+    const int r0 = tile % tiles_x * T::BX, o0 = tile / tiles_x * T::BW;
+    const int mine_x = min(rows - r0, T::BX), mine_w = min(out - o0, T::BW);
     const int xs = (int)x.code_stride, ws = (int)w.code_stride;
-    // what a load leaves out (rows past the end, blocks past the last) is asked
-    // for behind the buffer's end, where a load gives 0
-    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride), (short)0, (mine_x - 1) * xs + blocks * 16,
-        0x00020000);
-    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        uniform(static_cast<const char*>(w.codes) + o0 * w.code_stride), (short)0, (mine_w - 1) * ws + blocks * 16,
-        0x00020000);
-    constexpr int kNowhere = 0x7FFFFFF0;
-    const int lrow = tid >> 3, lblock = (tid & 7) ^ (lrow & 7);
-    auto fetch = [&](int turn, int stage) {
-        const bool in = turn * 8 + lblock < blocks;
-        const int col = (turn * 8 + lblock) * 16;
+    const int wave_w = wave % T::WW, wave_x = wave / T::WW;
+    Tiled<T> t{sh,
+               __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(w.codes) + o0 * w.code_stride),
+                                                 (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
+               __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride),
+                                                 (short)0, (mine_x - 1) * xs + blocks * 16, 0x00020000),
+               blocks, wave, (tid & 3) ^ (tid >> 4 & 3), {},
+               4 * (32 * T::TW * wave_w + (lane & 31)), 4 * (32 * T::TX * wave_x + (lane & 31)), lane >> 2 & 3,
+               lane >> 5, {}, {}};
 #pragma unroll
-        for (int u = 0; u < T::BM * 8 / T::kThreads; ++u) {
-            const int row = u * (T::kThreads / 8) + lrow;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64], 16,
-                                                     in && row < mine_x ? row * xs + col : kNowhere, 0, 0, 0);
-        }
+    for (int u = 0; u < T::kLoads; ++u) {
+        const int row = u * Tiled<T>::kLoadRows + (tid >> 2), in_x = row - T::BW;
+        t.from[u] = row < T::BW ? (row < mine_w ? (uint32_t)(row * ws + t.lblock * 16) : Tiled<T>::kNowhere)
+                                : (in_x < mine_x ? (uint32_t)(in_x * xs + t.lblock * 16) : Tiled<T>::kNowhere);
+    }
 #pragma unroll
-        for (int u = 0; u < T::BN * 8 / T::kThreads; ++u) {
-            const int row = u * (T::kThreads / 8) + lrow;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                wr, (lds_ptr)&sh.codes[stage][T::BM * 8 + u * T::kThreads + wave * 64], 16,
-                in && row < mine_w ? row * ws + col : kNowhere, 0, 0, 0);
-        }
-    };
-    // scales of 512 columns of a row: 16 bytes, through registers
-    constexpr int kScaleRows = (T::BM + T::BN) / T::kThreads;
-    static_assert(kScaleRows * T::kThreads == T::BM + T::BN, "a thread fetches the scales of whole rows");
-    u32x4 held[kScaleRows];
-    const uint8_t* sp[kScaleRows];
-#pragma unroll
-    for (int k = 0; k < kScaleRows; ++k) {
+    for (int k = 0; k < T::kScaleLoads; ++k) {
         const int row = k * T::kThreads + tid;
-        sp[k] = row < T::BM ? static_cast<const uint8_t*>(x.scales) + (r0 + min(row, mine_x - 1)) * x.scale_stride
-                            : static_cast<const uint8_t*>(w.scales) + (o0 + min(row - T::BM, mine_w - 1)) * w.scale_stride;
+        t.scale_row[k] =
+            row < T::BW ? static_cast<const uint8_t*>(w.scales) + (o0 + min(row, mine_w - 1)) * w.scale_stride
+                        : static_cast<const uint8_t*>(x.scales) + (r0 + min(row - T::BW, mine_x - 1)) * x.scale_stride;
     }
-    auto fetch_scales = [&](int pair) {
-        if ((pair + 1) * 16 <= blocks) {
+    f32x16 acc[T::TW][T::TX];
 #pragma unroll
-            for (int k = 0; k < kScaleRows; ++k) held[k] = *reinterpret_cast<const u32x4_u1*>(sp[k] + pair * 16);
-        } else {  // the last, byte by byte; nothing reads this half of sh.scales now
+    for (int i = 0; i < T::TW; ++i)
 #pragma unroll
-            for (int k = 0; k < kScaleRows; ++k) {
-                uint8_t* to = reinterpret_cast<uint8_t*>(&sh.scales[pair & 1][0][k * T::kThreads + tid]);
-                uint8_t b[16];
+        for (int j = 0; j < T::TX; ++j) acc[i][j] = f32x16{};
+
+    const int groups = (blocks + 15) / 16;  // of four turns; turns behind the last block multiply zeros
+    t.fetch_scales(0);
+    t.put_scales(0);
+    t.fetch(0, 0);
+    t.fetch(1, 1);
+    t.fetch(2, 2);
+    t.fetch(3, 3);
+    arrive<3 * T::kLoads>();
+    Step<T> f[2];
+    Scales<T> s[2];
+    t.read(0, 0, f[0]);
+    t.read_scales(0, 0, s[0]);
+    for (int g = 0; g < groups; ++g) {
+        // A turn's loads are asked for in order, so that waiting for all but the
+        // youngest two turns' leaves the next turn's there. The scales of the
+        // next group are asked for in the first turn and put down in the third;
+        // they are younger than two turns' loads until the fourth turn waits.
+        const int next = 4 * g + 4;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) b[i] = sp[k][min(pair * 16 + i, blocks - 1)];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    to[i / 4 * 4 * (T::BM + T::BN) + i % 4] = pair * 16 + i < blocks ? b[i] : (uint8_t)127;
-            }
+        for (int turn = 0; turn < 4; ++turn) {
+            t.read(turn, 1, f[1]);
+            t.template multiply<0>(f[0], s[turn & 1], acc);
+            __builtin_amdgcn_sched_barrier(0);
+            // the next turn's codes are there, and this one's have been read
+            if (turn == 1 || turn == 2)
+                arrive<2 * T::kLoads + T::kScaleLoads>();
+            else
+                arrive<2 * T::kLoads>();
+            if (turn == 0) t.fetch_scales(g + 1 < groups ? g + 1 : g);
+            if (turn == 2) t.put_scales(g + 1);
+            t.fetch(next + turn, turn);
+            t.read((turn + 1) & 3, 0, f[0]);
+            t.read_scales(turn == 3 ? g + 1 : g, (turn + 1) & 3, s[(turn + 1) & 1]);
+            t.template multiply<1>(f[1], s[turn & 1], acc);
+            __builtin_amdgcn_sched_barrier(0);
         }
-    };
-    auto put_scales = [&](int pair) {
-        if ((pair + 1) * 16 <= blocks) {
-#pragma unroll
-            for (int k = 0; k < kScaleRows; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sh.scales[pair & 1][i][k * T::kThreads + tid] = held[k][i];
-        }
-    };
-    f32x16 acc[T::TM][T::TN];
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) acc[i][j] = f32x16{};
-    const int wm = wave % T::WM, wn = wave / T::WM;
-    const int turns = (blocks + 7) / 8;
-    fetch(0, 0);
-    fetch_scales(0);
-    put_scales(0);
-    for (int t = 0; t < turns; ++t) {
-        __syncthreads();  // turn t's codes and scales are there, turn t - 1's no longer read
-        const int stage = t & 1, pair = t >> 1;
-        if (t + 1 < turns) fetch(t + 1, stage ^ 1);
-        if (stage == 0 && t + 2 < turns) fetch_scales(pair + 1);
-        uint32_t sx[T::TM], sw[T::TN];
-        const uint32_t* plane = sh.scales[pair & 1][2 * stage + half];
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i) sx[i] = plane[32 * (wm * T::TM + i) + (tid & 31)];
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) sw[j] = plane[T::BM + 32 * (wn * T::TN + j) + (tid & 31)];
-        const u32x4* xt = sh.codes[stage] + 32 * wm * T::TM * 8;
-        const u32x4* wt = sh.codes[stage] + (T::BM + 32 * wn * T::TN) * 8;
-        turn_step<T, 0>(xt, wt, sx, sw, half, acc);
-        turn_step<T, 1>(xt, wt, sx, sw, half, acc);
-        turn_step<T, 2>(xt, wt, sx, sw, half, acc);
-        turn_step<T, 3>(xt, wt, sx, sw, half, acc);
-        if (stage == 1 && t + 1 < turns) put_scales(pair + 1);
     }
-    // lane l has column l % 32 and rows 8 * (e / 4) + 4 * (l / 32) + e % 4
+    arrive<0>();  // the loads behind the last turn write shared memory, too
+    // Lane l has row l % 32 of y and columns 8 * (e / 4) + 4 * (l / 32) + e % 4.
+    const int row0 = r0 + 32 * T::TX * wave_x + (lane & 31);
+    const int col0 = o0 + 32 * T::TW * wave_w + 4 * (lane >> 5);
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i)
+    for (int j = 0; j < T::TX; ++j) {
+        if (row0 + 32 * j >= rows) continue;
+        char* at = static_cast<char*>(y) + ((row0 + 32 * j) * y_stride + col0) * (y_bf16 ? 2 : 4);
 #pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-            const int col = o0 + 32 * (wn * T::TN + j) + (tid & 31);
+        for (int i = 0; i < T::TW; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = r0 + 32 * (wm * T::TM + i) + 8 * (e / 4) + 4 * half + e % 4;
-                if (row < rows && col < out) store_y(y, y_bf16, row * y_stride + col, acc[i][j][e]);
+            for (int e = 0; e < 4; ++e) {
+                const int k = 32 * i + 8 * e;
+                const float v[4] = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+                store4(at, y_bf16, k, v, out - col0 - k);
             }
-        }
+    }
 }
 
 template <typename T>
 int launch_tiled(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
                  int64_t y_stride, hipStream_t s) {
-    const int64_t tm = (rows + T::BM - 1) / T::BM, tn = (out + T::BN - 1) / T::BN;
-    k_mx4_tiled<T><<<(unsigned)(tm * tn), T::kThreads, 0, s>>>(x, (int)rows, w, (int)out, (int)blocks, y, y_bf16, y_stride,
-                                                              (int)tm);
+    const int64_t tx = (rows + T::BX - 1) / T::BX, tw = (out + T::BW - 1) / T::BW;
+    k_mx4_tiled<T><<<(unsigned)(tx * tw), T::kThreads, 0, s>>>(x, (int)rows, w, (int)out, (int)blocks, y, y_bf16,
+                                                              y_stride, (int)tx);
     return (int)hipGetLastError();
 }
 
