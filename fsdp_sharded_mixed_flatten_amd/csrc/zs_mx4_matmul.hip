@@ -64,6 +64,18 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& x, uint32_t sx, const u32x4
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, kFp4, kFp4, 0, (int)sx, 0, (int)sw);
 }
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// 32 x 32 products of 64 columns, with byte STEP of each side's scales. Lane l gives
+// one block of row l % 32 of either side and has column l % 32 (x) and rows 8 (e / 4)
+// + 4 (l / 32) + e % 4 (W) of the result.
+template <int STEP>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& w, uint32_t sw, const u32x4& x, uint32_t sx, f32x16 acc) {
+    const i32x8 a{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    const i32x8 b{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFp4, kFp4, STEP, (int)sw, STEP, (int)sx);
+}
+
 // ------------------------------------------------------------------ any size
 // A workgroup computes 16 x 16 results; its waves take turns of 512 columns (16
 // blocks of either side, four matrix instructions) and add up through shared
@@ -132,6 +144,85 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4 x, int64_t rows,
     }
 }
 
+// Up to 32 TX rows of x, 32 rows of W: the waves of a workgroup take turns of 512
+// columns, whose operands they hold in registers (eight instructions of 64
+// columns, of which a lane of the upper half gives the second block), and add up
+// through shared memory.
+template <int TX>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_rows(Mx4 x, int rows, Mx4 w, int out, int blocks,
+                                                             void* __restrict__ y, int y_bf16, int64_t y_stride) {
+    __shared__ float part[kFewWaves][16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int r0 = blockIdx.y * 32 * TX, o0 = blockIdx.x * 32;
+    const int64_t o = min(o0 + (lane & 31), out - 1);
+    const char* wc = static_cast<const char*>(w.codes) + o * w.code_stride;
+    const uint8_t* ws = static_cast<const uint8_t*>(w.scales) + o * w.scale_stride;
+    const char* xc[TX];
+    const uint8_t* xs[TX];
+#pragma unroll
+    for (int j = 0; j < TX; ++j) {
+        const int64_t r = min(r0 + 32 * j + (lane & 31), rows - 1);
+        xc[j] = static_cast<const char*>(x.codes) + r * x.code_stride;
+        xs[j] = static_cast<const uint8_t*>(x.scales) + r * x.scale_stride;
+    }
+    f32x16 acc[TX];
+#pragma unroll
+    for (int j = 0; j < TX; ++j) acc[j] = f32x16{};
+    const int whole = blocks / 16;
+    for (int t = wave; t < whole; t += kFewWaves) {
+        u32x4 a[8], b[TX][8], sa, sb[TX];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            a[s] = *reinterpret_cast<const u32x4*>(wc + (int64_t)(t * 16 + 2 * s + half) * 16);
+        sa = *reinterpret_cast<const u32x4_u1*>(ws + t * 16);
+#pragma unroll
+        for (int j = 0; j < TX; ++j) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                b[j][s] = *reinterpret_cast<const u32x4*>(xc[j] + (int64_t)(t * 16 + 2 * s + half) * 16);
+            sb[j] = *reinterpret_cast<const u32x4_u1*>(xs[j] + t * 16);
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int j = 0; j < TX; ++j)
+                acc[j] = s & 1 ? mfma32<2>(a[s], sa[s / 2] >> (8 * half), b[j][s], sb[j][s / 2] >> (8 * half), acc[j])
+                               : mfma32<0>(a[s], sa[s / 2] >> (8 * half), b[j][s], sb[j][s / 2] >> (8 * half), acc[j]);
+    }
+    // the rest, two blocks at a time: what lies behind the last is 0 with scale 1
+    if (wave == whole % kFewWaves) {
+        for (int s = whole * 16; s < blocks; s += 2) {
+            const bool in = s + half < blocks;
+            const int at = in ? s + half : s;
+            u32x4 a = *reinterpret_cast<const u32x4*>(wc + (int64_t)at * 16);
+            if (!in) a = u32x4{0, 0, 0, 0};
+            const uint32_t sa = in ? ws[at] : 127u;
+#pragma unroll
+            for (int j = 0; j < TX; ++j) {
+                const u32x4 b = *reinterpret_cast<const u32x4*>(xc[j] + (int64_t)at * 16);
+                acc[j] = mfma32<0>(a, sa, b, in ? xs[j][at] : 127u, acc[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < TX; ++j) {
+        if (j > 0) __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[wave][e][lane] = acc[j][e];
+        __syncthreads();
+        // thread i has values 2 (i / 64) and the next of lane i % 64
+#pragma unroll
+        for (int q = 0; q < 16 / kFewWaves; ++q) {
+            const int e = (16 / kFewWaves) * wave + q;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kFewWaves; ++k) sum += part[k][e][lane];
+            const int row = r0 + 32 * j + (lane & 31), col = o0 + 8 * (e / 4) + 4 * half + e % 4;
+            if (row < rows && col < out) store_y(y, y_bf16, row * y_stride + col, sum);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ many rows
 // A workgroup computes BW columns of y (rows of W) for BX rows of x, its WW x WX
 // waves 32 TW x 32 TX each. Both sides' codes go straight from global to shared
@@ -145,30 +236,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4 x, int64_t rows,
 // lane's two scales are neighbouring bytes, which the instruction's operand
 // selection picks. W gives the rows of an instruction's result, so that a lane
 // holds four columns of y side by side.
-template <int TW_, int TX_, int WW_, int WX_>
+template <int TW_, int TX_, int WW_, int WX_, int BLOCKS_, int STAGES_, int PER_SIMD_>
 struct Tile {
-    static constexpr int TW = TW_, TX = TX_, WW = WW_, WX = WX_;
+    static constexpr int TW = TW_, TX = TX_, WW = WW_, WX = WX_, kStages = STAGES_, kPerSimd = PER_SIMD_;
+    // 32-column blocks of a turn, 64-column steps of it, turns of a group of 512 columns
+    static constexpr int kBlocks = BLOCKS_, kSteps = BLOCKS_ / 2, kTurns = 16 / BLOCKS_;
     static constexpr int kThreads = 64 * WW * WX, BW = 32 * TW * WW, BX = 32 * TX * WX, kRows = BW + BX;
-    static constexpr int kLoads = kRows * 4 / kThreads;  // 16-byte loads of a thread a turn
+    // 16-byte loads of a thread a turn, the same number in all waves: loads behind
+    // the last row are of nothing
+    static constexpr int kLoads = (kRows * kBlocks + kThreads - 1) / kThreads;
     static constexpr int kScaleLoads = (kRows + kThreads - 1) / kThreads;
-    static_assert(BW * 4 % kThreads == 0 && BX * 4 % kThreads == 0, "whole loads");
+    static_assert(BW * kBlocks % kThreads == 0, "a load is of one side");
+    static_assert(kBlocks == 4 || kBlocks == 8, "the layout of shared memory");
 };
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-template <int STEP>
-__device__ __forceinline__ f32x16 mfma32(const u32x4& w, uint32_t sw, const u32x4& x, uint32_t sx, f32x16 acc) {
-    const i32x8 a{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-    const i32x8 b{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFp4, kFp4, STEP, (int)sw, STEP, (int)sx);
-}
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 template <typename T>
 struct Shared {
-    u32x4 codes[4][T::kRows * 4];
-    uint32_t scales[2][4][T::kRows];  // of 512 columns, two of them in turn: a word a turn and row
+    u32x4 codes[T::kStages][T::kLoads * T::kThreads];
+    uint32_t scales[4][T::kRows];  // of 512 columns: a word a turn and row
 };
 
 // A pointer that is the same in every lane, in scalar registers.
@@ -194,9 +281,10 @@ struct Tiled {
     Shared<T>& sh;
     __amdgpu_buffer_rsrc_t wr, xr;
     int blocks;
+    bool once;                  // no other tile reads this one's rows of W
     int wave, lblock;           // the block of a turn that this thread's loads take
     uint32_t from[T::kLoads];   // and where in W and x they find it in turn 0
-    int read_w, read_x;      // the row of a tile whose blocks this lane reads, times 4
+    int read_w, read_x;      // the rows of the tile's sides whose blocks this lane reads first
     int swizzle, half;
     const uint8_t* scale_row[T::kScaleLoads];
     u32x4 held[T::kScaleLoads];
@@ -205,14 +293,23 @@ struct Tiled {
     // for behind the buffer's end, where a load gives 0. Buffers are shorter than
     // 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
     static constexpr uint32_t kNowhere = 0x7FFFFFF0u;
-    static constexpr int kLoadRows = T::kThreads / 4;
+    // W where no other tile reads its rows: whole lines that leave the cache to x and
+    // the scales, whose lines are read a piece at a time (20 rows x 8192 x 128256:
+    // 114 us against 125). With half lines a turn the other half would be lost.
+    static constexpr int kNontemporal = 2;
+    static constexpr int kLoadRows = T::kThreads / T::kBlocks;
     __device__ __forceinline__ void fetch(int turn, int stage) {
-        const uint32_t add = turn * 4 + lblock < blocks ? turn * 64u : kNowhere;
+        const uint32_t add = turn * T::kBlocks + lblock < blocks ? turn * (T::kBlocks * 16u) : kNowhere;
 #pragma unroll
-        for (int u = 0; u < T::kLoads; ++u)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(u < T::BW / kLoadRows ? wr : xr,
-                                                     (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64], 16,
-                                                     (int)(from[u] + add), 0, 0, 0);
+        for (int u = 0; u < T::kLoads; ++u) {
+            const lds_ptr to = (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64];
+            if (u >= T::BW / kLoadRows)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, (int)(from[u] + add), 0, 0, 0);
+            else if (T::kBlocks == 8 && once)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, (int)(from[u] + add), 0, 0, kNontemporal);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, (int)(from[u] + add), 0, 0, 0);
+        }
     }
     // Scales of 512 columns (16 bytes a row) go through registers.
     __device__ __forceinline__ void fetch_scales(int group) {
@@ -222,39 +319,45 @@ struct Tiled {
                 held[k] = *reinterpret_cast<const u32x4_u1*>(scale_row[k] + group * 16);
         } else {  // the last: what lies behind the row's end is 1
 #pragma unroll
-            for (int k = 0; k < T::kScaleLoads; ++k) {
-                uint32_t b[16];
+            for (int k = 0; k < T::kScaleLoads; ++k)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) b[i] = scale_row[k][min(group * 16 + i, blocks - 1)];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t b[4];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) b[i] = group * 16 + i < blocks ? b[i] : 127;
+                    for (int e = 0; e < 4; ++e) b[e] = scale_row[k][min(group * 16 + 4 * i + e, blocks - 1)];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    held[k][i] = b[4 * i] | (b[4 * i + 1] << 8) | (b[4 * i + 2] << 16) | (b[4 * i + 3] << 24);
-            }
+                    for (int e = 0; e < 4; ++e) b[e] = group * 16 + 4 * i + e < blocks ? b[e] : 127;
+                    held[k][i] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+                }
         }
     }
-    __device__ __forceinline__ void put_scales(int group) {
+    // The words of turns FIRST to LAST.
+    template <int FIRST, int LAST>
+    __device__ __forceinline__ void put_scales() {
 #pragma unroll
         for (int k = 0; k < T::kScaleLoads; ++k) {
             const int row = k * T::kThreads + threadIdx.x;
             if (T::kRows % T::kThreads == 0 || row < T::kRows)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sh.scales[group & 1][i][row] = held[k][i];
+                for (int i = FIRST; i <= LAST; ++i) sh.scales[i][row] = held[k][i];
         }
     }
     __device__ __forceinline__ void read(int stage, int step, Step<T>& f) const {
-        const int place = (2 * half + step) ^ swizzle;
+        const int place = (T::kSteps * half + step) ^ swizzle;
+        constexpr int kUp = 32 * T::kBlocks;
 #pragma unroll
-        for (int i = 0; i < T::TW; ++i) f.w[i] = sh.codes[stage][read_w + 128 * i + place];
+        for (int i = 0; i < T::TW; ++i) f.w[i] = sh.codes[stage][read_w * T::kBlocks + kUp * i + place];
 #pragma unroll
-        for (int i = 0; i < T::TX; ++i) f.x[i] = sh.codes[stage][4 * T::BW + read_x + 128 * i + place];
+        for (int i = 0; i < T::TX; ++i) f.x[i] = sh.codes[stage][(T::BW + read_x) * T::kBlocks + kUp * i + place];
     }
-    __device__ __forceinline__ void read_scales(int group, int turn, Scales<T>& s) const {
+    // A lane's scales of a turn, the first step's in the lowest byte.
+    __device__ __forceinline__ void read_scales(int turn, Scales<T>& s) const {
+        const uint32_t* words = sh.scales[T::kBlocks == 4 ? turn : 2 * turn + half];
+        const int shift = T::kBlocks == 4 ? 16 * half : 0;
 #pragma unroll
-        for (int i = 0; i < T::TW; ++i) s.w[i] = sh.scales[group & 1][turn][read_w / 4 + 32 * i] >> (16 * half);
+        for (int i = 0; i < T::TW; ++i) s.w[i] = words[read_w + 32 * i] >> shift;
 #pragma unroll
-        for (int i = 0; i < T::TX; ++i) s.x[i] = sh.scales[group & 1][turn][T::BW + read_x / 4 + 32 * i] >> (16 * half);
+        for (int i = 0; i < T::TX; ++i) s.x[i] = words[T::BW + read_x + 32 * i] >> shift;
     }
     template <int STEP>
     __device__ __forceinline__ void multiply(const Step<T>& f, const Scales<T>& s, f32x16 (&acc)[T::TW][T::TX]) const {
@@ -262,6 +365,15 @@ struct Tiled {
         for (int i = 0; i < T::TW; ++i)
 #pragma unroll
             for (int j = 0; j < T::TX; ++j) acc[i][j] = mfma32<STEP>(f.w[i], s.w[i], f.x[j], s.x[j], acc[i][j]);
+    }
+    // All steps of a turn but the last, whose operands are read.
+    template <int STEP>
+    __device__ __forceinline__ void steps(int stage, Step<T> (&f)[2], const Scales<T>& s,
+                                          f32x16 (&acc)[T::TW][T::TX]) const {
+        read(stage, STEP + 1, f[(STEP + 1) & 1]);
+        multiply<STEP>(f[STEP & 1], s, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (STEP + 2 < T::kSteps) steps<STEP + 1>(stage, f, s, acc);
     }
 };
 
@@ -273,7 +385,7 @@ __device__ __forceinline__ void arrive() {
 }
 
 template <typename T>
-__global__ __launch_bounds__(T::kThreads) void k_mx4_tiled(Mx4 x, int rows, Mx4 w, int out, int blocks,
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void k_mx4_tiled(Mx4 x, int rows, Mx4 w, int out, int blocks,
                                                            void* __restrict__ y, int y_bf16, int64_t y_stride,
                                                            int tiles_x) {
     __shared__ Shared<T> sh;
@@ -289,12 +401,13 @@ __global__ __launch_bounds__(T::kThreads) void k_mx4_tiled(Mx4 x, int rows, Mx4 
                                                  (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
                __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride),
                                                  (short)0, (mine_x - 1) * xs + blocks * 16, 0x00020000),
-               blocks, wave, (tid & 3) ^ (tid >> 4 & 3), {},
-               4 * (32 * T::TW * wave_w + (lane & 31)), 4 * (32 * T::TX * wave_x + (lane & 31)), lane >> 2 & 3,
+               blocks, tiles_x == 1, wave, (tid & (T::kBlocks - 1)) ^ (tid >> 4 & (T::kBlocks - 1)), {},
+               32 * T::TW * wave_w + (lane & 31), 32 * T::TX * wave_x + (lane & 31),
+               T::kBlocks == 4 ? lane >> 2 & 3 : lane >> 1 & 7,
                lane >> 5, {}, {}};
 #pragma unroll
     for (int u = 0; u < T::kLoads; ++u) {
-        const int row = u * Tiled<T>::kLoadRows + (tid >> 2), in_x = row - T::BW;
+        const int row = u * Tiled<T>::kLoadRows + tid / T::kBlocks, in_x = row - T::BW;
         t.from[u] = row < T::BW ? (row < mine_w ? (uint32_t)(row * ws + t.lblock * 16) : Tiled<T>::kNowhere)
                                 : (in_x < mine_x ? (uint32_t)(in_x * xs + t.lblock * 16) : Tiled<T>::kNowhere);
     }
@@ -311,41 +424,51 @@ __global__ __launch_bounds__(T::kThreads) void k_mx4_tiled(Mx4 x, int rows, Mx4 
 #pragma unroll
         for (int j = 0; j < T::TX; ++j) acc[i][j] = f32x16{};
 
-    const int groups = (blocks + 15) / 16;  // of four turns; turns behind the last block multiply zeros
+    const int groups = (blocks + 15) / 16;  // turns behind the last block multiply zeros
     t.fetch_scales(0);
-    t.put_scales(0);
-    t.fetch(0, 0);
-    t.fetch(1, 1);
-    t.fetch(2, 2);
-    t.fetch(3, 3);
-    arrive<3 * T::kLoads>();
+#pragma unroll
+    for (int i = 0; i < T::kStages; ++i) t.fetch(i, i);
+    t.template put_scales<0, 3>();
+    if (T::kTurns == 2) t.fetch_scales(groups > 1 ? 1 : 0);
+    // all but the youngest kStages - 1 turns' loads (and the scales')
+    arrive<(T::kStages - 1) * T::kLoads>();
     Step<T> f[2];
     Scales<T> s[2];
     t.read(0, 0, f[0]);
-    t.read_scales(0, 0, s[0]);
+    t.read_scales(0, s[0]);
+    int at = 0;  // the present turn's stage
     for (int g = 0; g < groups; ++g) {
         // A turn's loads are asked for in order, so that waiting for all but the
-        // youngest two turns' leaves the next turn's there. The scales of the
-        // next group are asked for in the first turn and put down in the third;
-        // they are younger than two turns' loads until the fourth turn waits.
-        const int next = 4 * g + 4;
+        // youngest kStages - 2 turns' leaves the next turn's there. Of four turns,
+        // the first asks for the next group's scales, between the loads of turns
+        // kStages - 1 and kStages; of two, the second for those of the one after
+        // next. They are put down when the words they replace have been read.
 #pragma unroll
-        for (int turn = 0; turn < 4; ++turn) {
-            t.read(turn, 1, f[1]);
-            t.template multiply<0>(f[0], s[turn & 1], acc);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int turn = 0; turn < T::kTurns; ++turn) {
+            constexpr bool kFixed = T::kTurns % T::kStages == 0;
+            const int stage = kFixed ? turn % T::kStages : at;
+            const int then = kFixed ? (turn + 1) % T::kStages : (at + 1 == T::kStages ? 0 : at + 1);
+            t.template steps<0>(stage, f, s[turn & 1], acc);
             // the next turn's codes are there, and this one's have been read
-            if (turn == 1 || turn == 2)
-                arrive<2 * T::kLoads + T::kScaleLoads>();
+            if (T::kTurns == 4 && turn >= 1 && turn <= T::kStages - 2)
+                arrive<(T::kStages - 2) * T::kLoads + T::kScaleLoads>();
             else
-                arrive<2 * T::kLoads>();
-            if (turn == 0) t.fetch_scales(g + 1 < groups ? g + 1 : g);
-            if (turn == 2) t.put_scales(g + 1);
-            t.fetch(next + turn, turn);
-            t.read((turn + 1) & 3, 0, f[0]);
-            t.read_scales(turn == 3 ? g + 1 : g, (turn + 1) & 3, s[(turn + 1) & 1]);
-            t.template multiply<1>(f[1], s[turn & 1], acc);
+                arrive<(T::kStages - 2) * T::kLoads>();
+            if constexpr (T::kTurns == 4) {
+                if (turn == 0) t.fetch_scales(g + 1 < groups ? g + 1 : g);
+                if (turn == 2) t.template put_scales<0, 2>();
+                if (turn == 3) t.template put_scales<3, 3>();
+            } else {
+                if (turn == 0) t.template put_scales<0, 1>();
+                if (turn == 1) t.template put_scales<2, 3>();
+                if (turn == 1) t.fetch_scales(g + 2 < groups ? g + 2 : g);
+            }
+            t.fetch(T::kTurns * g + turn + T::kStages, stage);
+            t.read(then, 0, f[0]);
+            t.read_scales((turn + 1) % T::kTurns, s[(turn + 1) & 1]);
+            t.template multiply<T::kSteps - 1>(f[1], s[turn & 1], acc);
             __builtin_amdgcn_sched_barrier(0);
+            at = then;
         }
     }
     arrive<0>();  // the loads behind the last turn write shared memory, too
@@ -376,17 +499,10 @@ int launch_tiled(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t 
     return (int)hipGetLastError();
 }
 
-}  // namespace
-
-int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_features, int64_t blocks, void* y,
-                      int y_dtype, int64_t y_stride, void* stream) {
-    const hipStream_t s = static_cast<hipStream_t>(stream);
-    const int esz = y_dtype == ZS_DTYPE_BF16 ? 2 : 4;
-    if (rows > 64 && blocks > 0 && x.code_stride <= (1 << 22) && w.code_stride <= (1 << 22))
-        return launch_tiled<Tile<4, 4, 2, 2>>(x, rows, w, out_features, blocks, y, y_dtype == ZS_DTYPE_BF16, y_stride,
-                                              s);
+int launch_few(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
+               int64_t y_stride, hipStream_t s) {
     // a launch covers at most 2^32 - 1 work-items and 65535 tiles of rows
-    const int64_t tiles = (out_features + 15) / 16;
+    const int64_t tiles = (out + 15) / 16;
     const int64_t fit = ((int64_t(1) << 32) - 1) / (tiles * 64 * kFewWaves);
     const int64_t most = 16 * (fit < 1 ? 1 : fit > 65535 ? 65535 : fit);
     for (int64_t lo = 0; lo < rows; lo += most) {
@@ -394,11 +510,71 @@ int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_feat
         const Mx4 part{static_cast<const char*>(x.codes) + lo * x.code_stride,
                        static_cast<const char*>(x.scales) + lo * x.scale_stride, x.code_stride, x.scale_stride};
         k_mx4_few<<<dim3((unsigned)tiles, (unsigned)((n + 15) / 16)), 64 * kFewWaves, 0, s>>>(
-            part, n, w, out_features, (int)blocks, static_cast<char*>(y) + lo * y_stride * esz,
-            y_dtype == ZS_DTYPE_BF16, y_stride);
+            part, n, w, out, (int)blocks, static_cast<char*>(y) + lo * y_stride * (y_bf16 ? 2 : 4), y_bf16, y_stride);
         if (hipError_t e = hipGetLastError()) return (int)e;
     }
     return 0;
+}
+
+template <int TX>
+int launch_rows(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
+                int64_t y_stride, hipStream_t s) {
+    k_mx4_rows<TX><<<dim3((unsigned)((out + 31) / 32), (unsigned)((rows + 32 * TX - 1) / (32 * TX))), 64 * kFewWaves, 0,
+                     s>>>(x, (int)rows, w, (int)out, (int)blocks, y, y_bf16, y_stride);
+    return (int)hipGetLastError();
+}
+
+// 128 columns of y for 64 rows of x: three stages of 256 columns.
+using Narrow = Tile<2, 1, 2, 2, 8, 3, 2>;
+// 128 for 128: four stages of 128 columns, two workgroups a compute unit.
+using Middle = Tile<2, 2, 2, 2, 4, 4, 2>;
+// 256 for 256: eight waves, the fewest bytes through shared memory a flop.
+using Wide = Tile<2, 4, 4, 2, 4, 4, 2>;
+
+enum Shape { kFew, kRows, kNarrow, kMiddle, kWide };
+
+// The shape for rows of x and out rows of W, by how many workgroups each gives the
+// 256 compute units. us, columns x rows of W:
+//   rows of x                   few  rows<2>  narrow  middle  wide
+//   1, 8192 x 128256            111      168     105     115   131
+//   16, 8192 x 28672             41       50      32      32    51   narrow from 200 tiles on
+//   16, 4096 x 4096             4.5      6.7      10      11    23
+//   20, 2048 x 11008            8.7      9.0     6.5     7.6    14   above 16 rows from 80 on
+//   20, 28672 x 8192             63       43      83      79   155
+//   64, 28672 x 8192            133       70      90      87   168
+//   77, 28672 x 8192            162       98      74      88   170   narrow up to 256 tiles
+//   192, 2048 x 11008            36       27      14      11    20
+//   256, 8192 x 28672           495      234      97      66    74   wide from 160 tiles on
+//   384, 8192 x 28672                            144      94    77
+//   1024, 2048 x 11008                            33      29    27
+Shape choose(int64_t rows, int64_t out) {
+    const int64_t narrow = (out + Narrow::BW - 1) / Narrow::BW;
+    if (rows <= Narrow::BX) {
+        if (narrow >= 200 || (rows > 16 && narrow >= 80)) return kNarrow;
+        return rows <= 16 ? kFew : kRows;
+    }
+    const int64_t wide = ((rows + Wide::BX - 1) / Wide::BX) * ((out + Wide::BW - 1) / Wide::BW);
+    if (rows > Middle::BX && wide >= 160) return kWide;
+    return ((rows + Narrow::BX - 1) / Narrow::BX) * narrow <= 256 ? kNarrow : kMiddle;
+}
+
+// Offsets in a tile stay below 2^30: 256 rows of 2^22 bytes (2^23 columns).
+constexpr int64_t kTiledStride = int64_t(1) << 22;
+
+}  // namespace
+
+int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_features, int64_t blocks, void* y,
+                      int y_dtype, int64_t y_stride, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int bf16 = y_dtype == ZS_DTYPE_BF16;
+    const bool tiled = blocks > 0 && x.code_stride <= kTiledStride && w.code_stride <= kTiledStride;
+    switch (tiled ? choose(rows, out_features) : kFew) {
+        case kRows: return launch_rows<2>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        case kNarrow: return launch_tiled<Narrow>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        case kMiddle: return launch_tiled<Middle>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        case kWide: return launch_tiled<Wide>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        default: return launch_few(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+    }
 }
 
 }  // namespace zs

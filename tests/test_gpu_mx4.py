@@ -259,6 +259,21 @@ def test_exact_products_by_columns(zs, cols):
         _check(zs, rows, out, cols, "f32", cols, None)
 
 
+@pytest.mark.parametrize("rows,out", [(1, 25473), (16, 25500), (17, 10113), (20, 30001), (33, 10200), (64, 25600),
+                                      (65, 8200), (65, 16390), (128, 16500), (130, 16384), (129, 40800), (257, 20481),
+                                      (300, 20600), (512, 20992)])
+def test_exact_products_of_many_tiles(zs, rows, out):
+    """Sizes at which there are tiles enough for every larger shape of workgroup, and one fewer or more."""
+    for cols in (32, 288, 1055, 1600):
+        _check(zs, rows, out, cols, "f32", rows, None)
+
+
+@pytest.mark.parametrize("rows,out", [(20, 26000), (100, 17000), (300, 21000)])
+def test_products_of_many_tiles(zs, rows, out):
+    for dtype in ("bf16", "f32"):
+        _check(zs, rows, out, 1216, dtype, 7, (120, 134), pad=1, shift=1, y_pad=3)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,out,cols", [(1, 4096, 4096), (3, 65, 8192), (20, 1003, 1536), (48, 256, 2048),
                                            (77, 503, 1531), (130, 384, 1024), (300, 520, 4096), (1024, 1024, 512)])
@@ -274,7 +289,7 @@ def test_strides(zs, rows, out, cols):
         _check(zs, rows, out, cols, "bf16", 5, (125, 129), pad, shift, y_pad)
 
 
-@pytest.mark.parametrize("rows,out", [(2, 20), (40, 60), (150, 140), (300, 270)])
+@pytest.mark.parametrize("rows,out", [(2, 20), (40, 60), (150, 140), (300, 270), (3, 25600), (70, 16400), (260, 20500)])
 def test_nan_blocks_infinities_and_zeros(zs, rows, out):
     """A NaN scale reaches every result of its row and no other; products past fp32's range are infinite; what is below
     its normal range may be 0."""
