@@ -9,11 +9,13 @@
 
 namespace zs {
 
-// Logits of a row that one workgroup sums.
-constexpr int64_t kVerifyChunk = 8192;
+// Logits of a row that one wave sums, where there are pieces enough for every wave
+// that the GPU runs at once on one of its 1024 SIMDs, and where there are not.
+constexpr int32_t kVerifyPiece = 2048, kVerifySmallPiece = 512;
+constexpr int64_t kVerifyManyPieces = 1024;
 
-// Largest logit of a chunk and the sum of its exponentials relative to that
-// logit, in 64 bits. A NaN or +infinity in the chunk: top is NaN.
+// Largest logit of a piece (NaN: there is a NaN or +infinity in it) and the sum of
+// its exponentials relative to that logit, in 64 bits.
 struct VerifyPart {
     double top, sum;
 };
@@ -28,17 +30,23 @@ struct VerifyPick {
 };
 enum VerifyKind : int32_t { kDrawNothing = 0, kDrawTarget = 1, kDrawRest = 2 };
 
-// The workspace: parts [rows, chunks], the target's rows before the drafts';
-// totals [requests, chunks]; picks [requests].
+// The workspace: parts [rows, pieces], the target's rows before the drafts';
+// totals [requests, pieces]; picks [requests].
 struct VerifyLayout {
-    int64_t chunks, rows, totals_off, picks_off, bytes;
+    int32_t piece;
+    int64_t pieces, rows, totals_off, picks_off, bytes;
 };
 inline VerifyLayout verify_layout(int64_t requests, int32_t drafts, int64_t vocab) {
     VerifyLayout l;
-    l.chunks = (vocab + kVerifyChunk - 1) / kVerifyChunk;
     l.rows = requests * (2 * (int64_t)drafts + 1);
-    l.totals_off = l.rows * l.chunks * (int64_t)sizeof(VerifyPart);
-    l.picks_off = l.totals_off + (requests * l.chunks * 8 + 15) / 16 * 16;
+    const int64_t large = (vocab + kVerifyPiece - 1) / kVerifyPiece;
+    l.piece = l.rows * large >= kVerifyManyPieces ? kVerifyPiece : kVerifySmallPiece;
+    l.pieces = (vocab + l.piece - 1) / l.piece;
+    l.totals_off = l.rows * l.pieces * (int64_t)sizeof(VerifyPart);
+    l.picks_off = l.totals_off + requests * l.pieces * 8;
+    // a workspace serves every smaller call, the ones of small pieces too
+    constexpr int64_t small = kVerifyManyPieces * (kVerifyPiece / kVerifySmallPiece) * (int64_t)(sizeof(VerifyPart) + 8);
+    if (l.piece == kVerifyPiece && l.picks_off < small) l.picks_off = small;
     l.bytes = l.picks_off + requests * (int64_t)sizeof(VerifyPick);
     return l;
 }

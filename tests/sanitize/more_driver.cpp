@@ -75,13 +75,25 @@ void largest_extents() {
     const int64_t most = zs_verify_drafts_workspace_bytes(((int64_t(1) << 22) - 1) / 65, 64, int64_t(1) << 30);
     CHECK(most > 0 && most < int64_t(1) << 50);
     CHECK(zs_verify_drafts_workspace_bytes((int64_t(1) << 22) - 1, 0, int64_t(1) << 30) > 0);
-    for (int64_t v : {int64_t(1), zs::kVerifyChunk, zs::kVerifyChunk + 1}) {
-        const zs::VerifyLayout l = zs::verify_layout(3, 2, v);
-        CHECK(l.chunks == (v + zs::kVerifyChunk - 1) / zs::kVerifyChunk && l.rows == 15);
-        CHECK(l.totals_off == l.rows * l.chunks * (int64_t)sizeof(zs::VerifyPart));
-        CHECK(l.picks_off % 16 == 0 && l.picks_off >= l.totals_off + 3 * l.chunks * 8);
-        CHECK(l.bytes == l.picks_off + 3 * (int64_t)sizeof(zs::VerifyPick));
-    }
+    for (int64_t requests : {1, 3, 4096})
+        for (int64_t v : {1, 512, 513, 2048, 2049, 151936}) {
+            const zs::VerifyLayout l = zs::verify_layout(requests, 2, v);
+            CHECK(l.rows == requests * 5 && (l.piece == zs::kVerifyPiece || l.piece == zs::kVerifySmallPiece));
+            CHECK(l.pieces * l.piece >= v && (l.pieces - 1) * l.piece < v);
+            CHECK(l.totals_off == l.rows * l.pieces * (int64_t)sizeof(zs::VerifyPart));
+            CHECK(l.totals_off % 8 == 0 && l.picks_off % 8 == 0 && l.picks_off >= l.totals_off + requests * l.pieces * 8);
+            CHECK(l.bytes == l.picks_off + requests * (int64_t)sizeof(zs::VerifyPick));
+        }
+    // a workspace serves the smaller calls
+    for (int64_t requests = 1; requests < 3000; requests += 1 + requests / 5)
+        for (int32_t drafts : {0, 1, 2, 5, 64})
+            for (int64_t v = 1; v < 200000; v += 1 + v / 3) {
+                const int64_t here = zs_verify_drafts_workspace_bytes(requests, drafts, v);
+                CHECK(here <= zs_verify_drafts_workspace_bytes(requests + 1, drafts, v));
+                CHECK(here <= zs_verify_drafts_workspace_bytes(requests, drafts + (drafts < 64), v));
+                CHECK(here <= zs_verify_drafts_workspace_bytes(requests, drafts, v + 1));
+                CHECK(here <= zs_verify_drafts_workspace_bytes(requests, drafts, v + v / 3));
+            }
     before = zs::g_launches;
     const int64_t kRows = (int64_t(1) << 22) - 1, kStride = int64_t(1) << 38, kVocab = int64_t(1) << 30;
     const int64_t bytes = zs_verify_drafts_workspace_bytes(kRows, 0, kVocab);
