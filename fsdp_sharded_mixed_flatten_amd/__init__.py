@@ -693,19 +693,19 @@ def zs_grad_stats_multi(plan, sumsq_out, nonfinite_out, workspace, stats_workspa
     sumsq_out: CUDA float64 tensor (>= 1 element); nonfinite_out: CUDA int32
     tensor; stats_workspace: CUDA uint8 tensor of
     zs_grad_stats_multi_workspace_bytes."""
-    _check(_lib.zs_grad_stats_multi(plan.handle, workspace.data_ptr(), _scalar_ptr(sumsq_out, "float64", "sumsq_out"),
-                                    _scalar_ptr(nonfinite_out, "int32", "nonfinite_out"),
-                                    _ptr(stats_workspace, "bytes", 0, "stats_workspace"), stats_workspace.numel(),
-                                    _stream(stream)))
+    device = _lm_device(workspace, "workspace")
+    _lm_call(_lib.zs_grad_stats_multi, device, stream, plan.handle, workspace.data_ptr(),
+             _scalar_ptr(sumsq_out, "float64", "sumsq_out"), _scalar_ptr(nonfinite_out, "int32", "nonfinite_out"),
+             _ptr(stats_workspace, "bytes", 0, "stats_workspace"), stats_workspace.numel())
 
 
 def zs_adamw_shard_step_multi_clip(plan, hps, workspace, scale=None, skip=None, stream=None):
     """The multi-tensor AdamW step from the gradient times *scale, left out
     where *skip is set. hps: one set of hyperparameters per group."""
     arr, n = _hp_array(hps)
-    _check(_lib.zs_adamw_shard_step_multi_clip(plan.handle, arr, n, _scalar_ptr(scale, "float32", "scale"),
-                                               _scalar_ptr(skip, "int32", "skip"), workspace.data_ptr(),
-                                               _stream(stream)))
+    device = _lm_device(workspace, "workspace")
+    _lm_call(_lib.zs_adamw_shard_step_multi_clip, device, stream, plan.handle, arr, n,
+             _scalar_ptr(scale, "float32", "scale"), _scalar_ptr(skip, "int32", "skip"), workspace.data_ptr())
 
 
 # ---------------------------------------------------------------- scalars in device memory
