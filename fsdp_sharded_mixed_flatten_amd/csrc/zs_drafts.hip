@@ -201,30 +201,44 @@ __global__ __launch_bounds__(kThreads) void k_verify_rows(VerifyArgs a, Scale sc
     if ((threadIdx.x & 63) == 0) parts[row * pieces + piece] = VerifyPart{top64, sum};
 }
 
-// A row's largest logit and sum, from its pieces', by kJoin lanes; bad rows have
-// a NaN for the largest.
-constexpr int kJoin = 16;
+// A row's largest logit and sum, from its pieces', by kJoin lanes that take kHeld
+// pieces at a time; bad rows have a NaN for the largest.
+constexpr int kJoin = 16, kHeld = 8;
 __device__ __forceinline__ VerifyPart join(const Exp2& exp2, const VerifyPart* parts, int64_t pieces, bool any) {
     const int lane = threadIdx.x % kJoin;
-    double top = -kInf;
+    double top = -kInf, sum = 0.0;
     int bad = 0;
-    if (any)
-        for (int64_t c = lane; c < pieces; c += kJoin) {
-            const double t = parts[c].top;
-            bad |= !(t < kInf);
-            top = fmax(top, t);
+    for (int64_t c0 = 0; any && c0 < pieces; c0 += kJoin * kHeld) {
+        VerifyPart held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = c0 + i * kJoin + lane;
+            held[i] = parts[c < pieces ? c : c0];
+            if (c >= pieces) held[i] = VerifyPart{-kInf, 0.0};
         }
+        double most = top;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            bad |= !(held[i].top < kInf);
+            most = fmax(most, held[i].top);
+        }
+        if (!bad && most > -kInf) {
+            sum *= exp2(top - most);  // 0 where top is still -infinity
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) sum += held[i].sum * exp2(held[i].top - most);
+        }
+        top = most;
+    }
+    double all = top;
 #pragma unroll
     for (int d = kJoin / 2; d; d >>= 1) {
-        top = fmax(top, __shfl_xor(top, d, 64));
+        all = fmax(all, __shfl_xor(all, d, 64));
         bad |= __shfl_xor(bad, d, 64);
     }
-    double sum = 0.0;
-    if (any && !bad && top > -kInf)
-        for (int64_t c = lane; c < pieces; c += kJoin) sum += parts[c].sum * exp2(parts[c].top - top);
+    sum = !bad && all > -kInf ? sum * exp2(top - all) : 0.0;
 #pragma unroll
     for (int d = kJoin / 2; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    return VerifyPart{bad ? __builtin_nan("") : top, sum};
+    return VerifyPart{bad ? __builtin_nan("") : all, sum};
 }
 
 // ------------------------------------------------------------------ 2: what stands, and the rest

@@ -9,10 +9,15 @@
 
 namespace zs {
 
-// Logits of a row that one wave sums, where there are pieces enough for every wave
-// that the GPU runs at once on one of its 1024 SIMDs, and where there are not.
+// Logits of a row that one wave sums: large pieces where there are many of them,
+// small ones where waves are few and each one's time counts, and for short rows.
+// us of a call with 4 drafts in bf16, large and small pieces:
+//   1 x 32000    25  12     1 x 151936   15  17    256 x 32000    84 102
+//   8 x 32000    27  16     4 x 151936   25  21    16 x 100000    38  32
+//   64 x 32000   41  34     8 x 151936   30  30    32 x 65536     34  34
+//   128 x 32000  56  58    16 x 151936   40  44    300 x 500      30  17 (2 drafts)
 constexpr int32_t kVerifyPiece = 2048, kVerifySmallPiece = 512;
-constexpr int64_t kVerifyManyPieces = 1024;
+constexpr int64_t kVerifyManyPieces = 8192;
 
 // Largest logit of a piece (NaN: there is a NaN or +infinity in it) and the sum of
 // its exponentials relative to that logit, in 64 bits.
@@ -40,12 +45,13 @@ inline VerifyLayout verify_layout(int64_t requests, int32_t drafts, int64_t voca
     VerifyLayout l;
     l.rows = requests * (2 * (int64_t)drafts + 1);
     const int64_t large = (vocab + kVerifyPiece - 1) / kVerifyPiece;
-    l.piece = l.rows * large >= kVerifyManyPieces ? kVerifyPiece : kVerifySmallPiece;
+    l.piece = vocab >= kVerifyPiece && l.rows * large >= kVerifyManyPieces ? kVerifyPiece : kVerifySmallPiece;
     l.pieces = (vocab + l.piece - 1) / l.piece;
     l.totals_off = l.rows * l.pieces * (int64_t)sizeof(VerifyPart);
     l.picks_off = l.totals_off + requests * l.pieces * 8;
     // a workspace serves every smaller call, the ones of small pieces too
-    constexpr int64_t small = kVerifyManyPieces * (kVerifyPiece / kVerifySmallPiece) * (int64_t)(sizeof(VerifyPart) + 8);
+    const int64_t small = (l.rows > kVerifyManyPieces ? l.rows : kVerifyManyPieces) *
+                          (kVerifyPiece / kVerifySmallPiece) * (int64_t)(sizeof(VerifyPart) + 8);
     if (l.piece == kVerifyPiece && l.picks_off < small) l.picks_off = small;
     l.bytes = l.picks_off + requests * (int64_t)sizeof(VerifyPick);
     return l;

@@ -85,7 +85,7 @@ void largest_extents() {
             CHECK(l.bytes == l.picks_off + requests * (int64_t)sizeof(zs::VerifyPick));
         }
     // a workspace serves the smaller calls
-    for (int64_t requests = 1; requests < 3000; requests += 1 + requests / 5)
+    for (int64_t requests = 1; requests < 30000; requests += 1 + requests / 5)
         for (int32_t drafts : {0, 1, 2, 5, 64})
             for (int64_t v = 1; v < 200000; v += 1 + v / 3) {
                 const int64_t here = zs_verify_drafts_workspace_bytes(requests, drafts, v);

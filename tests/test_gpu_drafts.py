@@ -43,9 +43,10 @@ class Case:
         self.draft = logits(requests * k, target[:, :k] + 0.7 * rng.standard_normal((requests, k, vocab))) \
             if with_draft and k else None
         self.tokens = np.zeros((requests, k), np.int32)
+        drawn_from = self.draft64() if self.draft is not None else target
         for b in range(requests):
             for i in range(k):
-                p = drafts.softmax(self.draft64()[b, i] if with_draft else target[b, i], temperature)
+                p = drafts.softmax(drawn_from[b, i], temperature)
                 self.tokens[b, i] = np.searchsorted(np.cumsum(p), rng.random() * p.sum()).clip(0, vocab - 1)
         self.uniforms = rng.random((requests, k + 1)).astype(np.float32)
         self.lens = None if lens is None else np.asarray(lens, np.int32)

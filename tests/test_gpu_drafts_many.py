@@ -1,5 +1,5 @@
 """Verification of drafted tokens with rows enough to fill the GPU, where waves sum pieces of 2048 logits (few rows:
-of 512), against the same oracle and bounds as the small calls: 60 requests of 4 drafts are 540 rows."""
+of 512), against the same oracle and bounds as the small calls: 460 requests of 4 drafts are 4140 rows."""
 import math
 
 import numpy as np
@@ -9,21 +9,21 @@ from test_gpu_drafts import Case, zs  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 
-REQUESTS, K = 60, 4
+REQUESTS, K = 460, 4
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("with_draft", [True, False], ids=["draft", "certain"])
-@pytest.mark.parametrize("vocab", [2049, 4095, 4096, 4097, 6151])
+@pytest.mark.parametrize("vocab", [2049, 4096, 6151])
 def test_matches_the_oracle(zs, vocab, dtype, with_draft):
     lens = np.random.default_rng(vocab).integers(-1, K + 2, REQUESTS)
     Case(zs, REQUESTS, K, vocab, dtype, vocab, with_draft, lens=lens, temperature=1.3, pad=5, shift=1).run()
 
 
-@pytest.mark.parametrize("requests,k,vocab", [(341, 1, 2048), (342, 1, 2048), (1024, 0, 7), (1023, 0, 7), (2000, 0, 1),
-                                              (700, 1, 511), (700, 1, 513)])
+@pytest.mark.parametrize("requests,k,vocab", [(341, 1, 2048), (2730, 1, 2048), (2731, 1, 2048), (8192, 0, 2047),
+                                              (8191, 0, 7), (8193, 0, 1), (9000, 1, 513)])
 def test_where_the_pieces_change(zs, requests, k, vocab):
-    """1024 pieces are the border: a call on either side, and one of rows shorter than a piece."""
+    """8192 pieces are the border, and rows of 2048 logits: calls on either side."""
     Case(zs, requests, k, vocab, "f32", vocab).run()
 
 
@@ -59,19 +59,19 @@ def test_borders(zs):
     """Rows of four equal likelihoods, one in each piece and one at the end: a random number on a border of the powers
     of two belongs to the token behind it."""
     vocab, places = 8192, (5, 2048, 4099, 8191)
-    c = Case(zs, 300, 0, vocab, "f32", 4)
+    c = Case(zs, 2100, 0, vocab, "f32", 4)
     c.target.fill_(-math.inf)
     for j in places:
         c.target[:, j] = 1.5
-    c.uniforms[:, 0] = np.arange(300) % 8 / 8
+    c.uniforms[:, 0] = np.arange(2100) % 8 / 8
     c.run()
-    assert c.out[1].view(-1).tolist() == [places[i % 8 // 2] for i in range(300)]
+    assert c.out[1].view(-1).tolist() == [places[i % 8 // 2] for i in range(2100)]
 
 
 def test_a_workspace_serves_smaller_calls(zs):
     """The workspace of the largest call, given whole to smaller ones on both sides of the border."""
     big = Case(zs, REQUESTS, K, 6151, "bf16", 6).device()
-    for requests, k, vocab in ((1, 4, 6151), (60, 4, 500), (17, 3, 6151), (59, 4, 6151), (40, 4, 3001)):
+    for requests, k, vocab in ((1, 4, 6151), (460, 4, 500), (117, 3, 6151), (459, 4, 6151), (240, 4, 3001)):
         assert zs.zs_verify_drafts_workspace_bytes(requests, k, vocab) <= big.need
         c = Case(zs, requests, k, vocab, "f32", 7).device()
         c.work, c.need = big.work, big.need
