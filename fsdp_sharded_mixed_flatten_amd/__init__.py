@@ -214,6 +214,8 @@ def _check(status):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():  # what current_stream() gives, without its object
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -789,12 +791,13 @@ def _lm_rows(t, rows, cols, device, what):
     """Row stride of a [rows, cols] matrix whose rows are contiguous (its dtype is the caller's to check)."""
     if t.get_device() != device:
         raise _lm_elsewhere(t, device, what)
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if cols > 1 and col != 1:
         raise ValueError(f"{what} must have contiguous rows, its strides are {t.stride()}")
     # the stride of a single row is free, and may be anything in torch
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    return row if rows > 1 else max(cols, 1)
 
 
 def _lm_array(t, dtype, numel, cols, device, what):
@@ -854,7 +857,7 @@ def _lm_logits(logits):
         raise ValueError(f"logits must be bfloat16 or float32, got {dtype}")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, vocab], got {list(logits.shape)}")
-    rows, vocab = logits.size(0), logits.size(1)
+    rows, vocab = logits.shape
     return device, code, rows, vocab, _lm_rows(logits, rows, vocab, device, "logits")
 
 
@@ -972,7 +975,7 @@ def _mx4_conversion(x, codes, scales):
     code = _float_code(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must be [rows, cols], got {list(x.shape)}")
-    rows, cols = x.size(0), x.size(1)
+    rows, cols = x.shape
     return device, code, rows, cols, _lm_rows(x, rows, cols, device, "x"), \
         _mx4_matrix(codes, scales, rows, -(-cols // ZS_MX4_BLOCK), device, ("codes", "scales"))
 
@@ -997,7 +1000,8 @@ def zs_mx4_matmul(x_codes, x_scales, w_codes, w_scales, y, stream=None):
     if x_scales.dim() != 2 or w_scales.dim() != 2:
         raise ValueError(f"x_scales and w_scales must be matrices, got {list(x_scales.shape)} and "
                          f"{list(w_scales.shape)}")
-    rows, blocks, out = x_scales.size(0), x_scales.size(1), w_scales.size(0)
+    rows, blocks = x_scales.shape
+    out = w_scales.shape[0]
     x = _mx4_matrix(x_codes, x_scales, rows, blocks, device, ("x_codes", "x_scales"))
     w = _mx4_matrix(w_codes, w_scales, out, blocks, device, ("w_codes", "w_scales"))
     code = _float_code(y, "y")
@@ -1026,7 +1030,7 @@ def zs_verify_drafts(target_logits, draft_tokens, uniforms, accepted, tokens, wo
     device, code, places, vocab, stride = _lm_logits(target_logits)
     if draft_tokens.dim() != 2:
         raise ValueError(f"draft_tokens must be [requests, drafts], got {list(draft_tokens.shape)}")
-    requests, drafts = draft_tokens.size(0), draft_tokens.size(1)
+    requests, drafts = draft_tokens.shape
     if places != requests * (drafts + 1):
         raise ValueError(f"target_logits must have {requests * (drafts + 1)} rows, got {places}")
     i32, f32 = _torch.int32, _torch.float32
