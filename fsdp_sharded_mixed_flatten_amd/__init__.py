@@ -690,6 +690,14 @@ def zs_grad_stats_multi_workspace_bytes(plan):
     return _lib.zs_grad_stats_multi_workspace_bytes(plan.handle)
 
 
+def _scalar_on(device, t, dtype_name, what):
+    """_scalar_ptr of a tensor that has to be on the call's device."""
+    p = _scalar_ptr(t, dtype_name, what)
+    if t is not None and t.get_device() != device:
+        raise _lm_elsewhere(t, device, what)
+    return p
+
+
 def zs_grad_stats_multi(plan, sumsq_out, nonfinite_out, workspace, stats_workspace, stream=None):
     """Squared norm and non-finite flag of the grad pieces bound to workspace.
     sumsq_out: CUDA float64 tensor (>= 1 element); nonfinite_out: CUDA int32
@@ -697,8 +705,9 @@ def zs_grad_stats_multi(plan, sumsq_out, nonfinite_out, workspace, stats_workspa
     zs_grad_stats_multi_workspace_bytes."""
     device = _lm_device(workspace, "workspace")
     _lm_call(_lib.zs_grad_stats_multi, device, stream, plan.handle, workspace.data_ptr(),
-             _scalar_ptr(sumsq_out, "float64", "sumsq_out"), _scalar_ptr(nonfinite_out, "int32", "nonfinite_out"),
-             _ptr(stats_workspace, "bytes", 0, "stats_workspace"), stats_workspace.numel())
+             _scalar_on(device, sumsq_out, "float64", "sumsq_out"),
+             _scalar_on(device, nonfinite_out, "int32", "nonfinite_out"),
+             _lm_flat(stats_workspace, (_torch.uint8,), 0, device, "stats_workspace"), stats_workspace.numel())
 
 
 def zs_adamw_shard_step_multi_clip(plan, hps, workspace, scale=None, skip=None, stream=None):
@@ -707,7 +716,8 @@ def zs_adamw_shard_step_multi_clip(plan, hps, workspace, scale=None, skip=None, 
     arr, n = _hp_array(hps)
     device = _lm_device(workspace, "workspace")
     _lm_call(_lib.zs_adamw_shard_step_multi_clip, device, stream, plan.handle, arr, n,
-             _scalar_ptr(scale, "float32", "scale"), _scalar_ptr(skip, "int32", "skip"), workspace.data_ptr())
+             _scalar_on(device, scale, "float32", "scale"), _scalar_on(device, skip, "int32", "skip"),
+             workspace.data_ptr())
 
 
 # ---------------------------------------------------------------- scalars in device memory

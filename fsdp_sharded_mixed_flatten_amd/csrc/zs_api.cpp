@@ -1113,7 +1113,9 @@ zs_status bound_tables(const zs_plan* plan, const void* workspace, int32_t need,
     Binding b;
     if (zs_status st = lookup_binding(plan, workspace, need, &b)) return st;
     out->off = multi_offsets(plan, b.n_contribs);
-    out->unsummed = multi_layout(plan, b.n_contribs).unsummed_off;
+    const MultiLayout l = multi_layout(plan, b.n_contribs);
+    out->unsummed = l.unsummed_off;
+    out->bytes = l.total;
     return ZS_OK;
 }
 

@@ -28,9 +28,12 @@ zs_status zs_grad_stats_multi(const zs_plan* plan, const void* workspace, double
                       (long long)stats_workspace_bytes, (long long)need);
     const Span out[3] = {span(sumsq_out, 8), span(nonfinite_out, 4), span(stats_workspace, need)};
     const char* name[3] = {"sumsq_out", "nonfinite_out", "stats_workspace"};
-    for (int i = 0; i < 3; ++i)
+    const Span table = span(workspace, t.bytes);
+    for (int i = 0; i < 3; ++i) {
+        if (zs_status st = check_apart(out[i], table, name[i], "workspace")) return st;
         for (int j = i + 1; j < 3; ++j)
             if (zs_status st = check_apart(out[i], out[j], name[i], name[j])) return st;
+    }
     trace_call("zs_grad_stats_multi", plan, 0, 0, plan->S, stream);
     return report_hip(launch_multi_norm(workspace, t, (int64_t)plan->chunk_piece.size(), sumsq_out, nonfinite_out,
                                         stats_workspace, stream),

@@ -10,10 +10,11 @@
 namespace zs {
 
 // The tables of a bound workspace. unsummed: byte offset of one byte a piece, 1
-// where its squares are another rank's to count; 0: this rank counts all.
+// where its squares are another rank's to count; 0: this rank counts all. bytes:
+// of the whole binding.
 struct BoundTables {
     MultiOffsets off;
-    int64_t unsummed;
+    int64_t unsummed, bytes;
 };
 
 // zs_api.cpp: the tables of the binding in a workspace, after checking that it

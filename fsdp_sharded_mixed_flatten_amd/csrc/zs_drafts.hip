@@ -472,7 +472,7 @@ __global__ __launch_bounds__(kPiece / kDrawPer) void k_verify_draw(VerifyArgs a,
         if (whole || all > 0.0) break;
         whole = true;  // p nowhere exceeds q: drawn from p
     }
-    const double border = u * all;
+    const double border = u >= 1.0 ? kInf : u * all;  // from 1 on no rounding of a running sum passes it
     int owner = choose(mine, run, border, choices[0]);
     if ((int)threadIdx.x == owner) {
         int64_t found = c0;

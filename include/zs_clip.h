@@ -35,7 +35,8 @@ int64_t zs_grad_stats_multi_workspace_bytes(const zs_plan* plan);
  * squared norm of the whole gradient; its elements are looked at for the flag on
  * every rank. grad has to be bound. sumsq_out is 8-byte, nonfinite_out 4-byte
  * aligned; stats_workspace 16-byte, owned by the call while it is in flight, and
- * holding nothing between calls. */
+ * holding nothing between calls. The three overlap neither each other nor
+ * `workspace`. */
 zs_status zs_grad_stats_multi(const zs_plan* plan, const void* workspace, double* sumsq_out, int32_t* nonfinite_out,
                               void* stats_workspace, int64_t stats_workspace_bytes, void* stream);
 

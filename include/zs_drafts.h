@@ -22,7 +22,8 @@ extern "C" {
 /* Drafted tokens a request may have. */
 #define ZS_VERIFY_MAX_DRAFTS 64
 
-/* Device workspace bytes of zs_verify_drafts; -1 on a bad argument. */
+/* Device workspace bytes of zs_verify_drafts; -1 on a bad argument. They serve
+ * every call of no more requests, drafts and vocabulary. */
 int64_t zs_verify_drafts_workspace_bytes(int64_t requests, int32_t drafts, int64_t vocab);
 
 /* Request b has n_b = draft_lens[b] drafted tokens (draft_lens NULL: all have
@@ -43,8 +44,9 @@ int64_t zs_verify_drafts_workspace_bytes(int64_t requests, int32_t drafts, int64
  * Softmax, borders and running sums are computed in 64 bits, in which a token
  * less than 2^-1000 times as likely as the likeliest has probability 0. A logit
  * of -infinity is a masked token, never drawn; a drafted token outside [0,
- * vocab) falls, and without draft_logits takes nothing from p. u at or above 1 draws the last token that has
- * a probability, a negative or NaN u the first; a NaN u_i lets a token fall.
+ * vocab) falls, and without draft_logits takes nothing from p. u_drafts at or
+ * above 1 draws the last token that has a share, a negative or NaN one the
+ * first; a NaN u_i lets a token fall.
  *   draft_lens[b] < 0   the request is skipped: accepted 0, tokens -1,
  *                       logprobs 0; its rows do not matter.
  *   a NaN or +infinity in a row that is needed, or a needed target row of
@@ -52,8 +54,7 @@ int64_t zs_verify_drafts_workspace_bytes(int64_t requests, int32_t drafts, int64
  *                       the token -1 and its log-probability NaN.
  *   a draft row of -infinity alone   q = 0.
  * Logits are of one dtype; rows and strides as in zs_lm.h, with requests *
- * (drafts + 1) < 2^22; vocab in [1, 2^30], temperature (a double) in
- * [1e-6, 1e6],
+ * (drafts + 1) < 2^22; vocab in [1, 2^30], temperature in [1e-6, 1e6],
  * 0 <= drafts <= ZS_VERIFY_MAX_DRAFTS (0: one token is drawn from each row).
  * requests == 0 does nothing. draft_tokens and draft_logits may be NULL for
  * drafts == 0. workspace is 16-byte aligned. Outputs and workspace overlap

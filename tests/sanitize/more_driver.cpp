@@ -177,6 +177,9 @@ void clip_tables() {
             CHECK(zs_grad_stats_multi(p, w, sum, at<int32_t>(uint64_t(1) << 50), stats, sb, nullptr) == ZS_EINVAL);
             CHECK(zs_grad_stats_multi(p, w, at<double>(uint64_t(1) << 51), flag, stats, sb, nullptr) == ZS_EINVAL);
             CHECK(zs_grad_stats_multi(p, w, sum, flag, nullptr, sb, nullptr) == ZS_EINVAL);
+            CHECK(zs_grad_stats_multi(p, w, reinterpret_cast<double*>(w + need - 8), flag, stats, sb, nullptr) == ZS_EINVAL);
+            CHECK(zs_grad_stats_multi(p, w, sum, reinterpret_cast<int32_t*>(w), stats, sb, nullptr) == ZS_EINVAL);
+            CHECK(zs_grad_stats_multi(p, w, sum, flag, w, sb, nullptr) == ZS_EINVAL);
             zs_adamw_hparams hp{1e-4, 0.9, 0.95, 1e-8, 0.1, 1};
             const float* scale = at<float>(uint64_t(1) << 52);
             CHECK(zs_adamw_shard_step_multi_clip(p, &hp, 1, scale, nullptr, w, nullptr) == ZS_OK);
