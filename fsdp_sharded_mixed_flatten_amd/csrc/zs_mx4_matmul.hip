@@ -14,6 +14,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // 16 scale bytes at any address (the hardware takes unaligned vector loads).
 typedef u32x4 __attribute__((aligned(1))) u32x4_u1;
+typedef uint32_t __attribute__((aligned(1))) u32_u1;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -276,6 +277,11 @@ struct Scales {
     uint32_t w[T::TW], x[T::TX];
 };
 
+// What a load leaves out (rows past the end, blocks past the last) is asked
+// for behind the buffer's end, where a load gives 0. Buffers are shorter than
+// 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
+constexpr uint32_t kNowhere = 0x7FFFFFF0u;
+
 template <typename T>
 struct Tiled {
     Shared<T>& sh;
@@ -289,10 +295,6 @@ struct Tiled {
     const uint8_t* scale_row[T::kScaleLoads];
     u32x4 held[T::kScaleLoads];
 
-    // What a load leaves out (rows past the end, blocks past the last) is asked
-    // for behind the buffer's end, where a load gives 0. Buffers are shorter than
-    // 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
-    static constexpr uint32_t kNowhere = 0x7FFFFFF0u;
     // W where no other tile reads its rows: whole lines that leave the cache to x and
     // the scales, whose lines are read a piece at a time (20 rows x 8192 x 128256:
     // 114 us against 125). With half lines a turn the other half would be lost.
@@ -408,8 +410,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void k_mx4_tiled(Mx4 x, i
 #pragma unroll
     for (int u = 0; u < T::kLoads; ++u) {
         const int row = u * Tiled<T>::kLoadRows + tid / T::kBlocks, in_x = row - T::BW;
-        t.from[u] = row < T::BW ? (row < mine_w ? (uint32_t)(row * ws + t.lblock * 16) : Tiled<T>::kNowhere)
-                                : (in_x < mine_x ? (uint32_t)(in_x * xs + t.lblock * 16) : Tiled<T>::kNowhere);
+        t.from[u] = row < T::BW ? (row < mine_w ? (uint32_t)(row * ws + t.lblock * 16) : kNowhere)
+                                : (in_x < mine_x ? (uint32_t)(in_x * xs + t.lblock * 16) : kNowhere);
     }
 #pragma unroll
     for (int k = 0; k < T::kScaleLoads; ++k) {
@@ -516,6 +518,157 @@ int launch_few(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t bl
     return 0;
 }
 
+// ------------------------------------------------------------------ few rows, many of W
+// Up to 32 rows of x, 32 TW rows of W. The workgroup's WAVES waves share a row's
+// columns, 256 each in turn, so that together they read runs of WAVES * 128 bytes
+// of a row (runs of one line take the memory longer: W laid out tile by tile would
+// stream in 96 us where the narrow tile's runs of one line take 114). A wave's
+// columns are its own: codes go through its own ring of STAGES turns in shared
+// memory with waits by count and no barrier, scales through registers. At the
+// end the waves' sums are added up through shared memory.
+template <int TW_, int WAVES_, int STAGES_>
+struct Long {
+    static constexpr int TW = TW_, kWaves = WAVES_, kStages = STAGES_;
+    static constexpr int kThreads = 64 * WAVES_, BW = 32 * TW_, kRows = BW + 32;
+    static constexpr int kWLoads = BW / 8, kLoads = kRows / 8;  // of a wave a turn, 16 bytes a lane
+    static constexpr int kTurnLoads = kLoads + TW_ + 1;         // with the scales'
+    static constexpr int kQuarter = 16 * TW_ / WAVES_;          // values of a lane that a wave adds up
+    static_assert(kQuarter % 4 == 0, "whole stores");
+    static_assert((kStages - 1) * kTurnLoads < 64, "what a wait can count");
+};
+
+template <typename T>
+struct LongWave {
+    u32x4 (&ring)[T::kStages][T::kLoads * 64];
+    __amdgpu_buffer_rsrc_t wr, xr;
+    const uint8_t* scale_row[T::TW + 1];
+    uint32_t from[T::kLoads];
+    int blocks, lblock, half;
+
+    // Loads of W leave the caches to x and the scales, whose lines are read a piece
+    // at a time.
+    __device__ __forceinline__ void fetch(int slice, int stage, uint32_t (&scales)[T::TW + 1]) {
+        const int at_block = min(slice * 8 + 4 * half, blocks - 4);
+#pragma unroll
+        for (int i = 0; i <= T::TW; ++i) scales[i] = *reinterpret_cast<const u32_u1*>(scale_row[i] + at_block);
+#pragma unroll
+        for (int u = 0; u < T::kLoads; ++u) {
+            const lds_ptr to = (lds_ptr)&ring[stage][u * 64];
+            const int block = slice * 8 + (lblock ^ (4 * (u & 1)));
+            const uint32_t at = from[u] + (block < blocks ? slice * 128u : kNowhere);
+            if (u < T::kWLoads)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, (int)at, 0, 0, 2);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, (int)at, 0, 0, 0);
+        }
+    }
+    // Scales that reach behind the row's end were read from its last four on; what
+    // lies behind is 1.
+    __device__ __forceinline__ void mend(int slice, uint32_t (&scales)[T::TW + 1]) const {
+        const int over = min(max(slice * 8 + 4 * half - (blocks - 4), 0), 4);
+#pragma unroll
+        for (int i = 0; i <= T::TW; ++i)
+            scales[i] = (uint32_t)((uint64_t(0x7F7F7F7F) << 32 | scales[i]) >> (8 * over));
+    }
+    template <int STEP>
+    __device__ __forceinline__ void step(int stage, int lane, const uint32_t (&scales)[T::TW + 1],
+                                         f32x16 (&acc)[T::TW]) const {
+        const int place = (lane & 31) * 8 + ((4 * half + STEP) ^ (lane >> 1 & 7));
+        const u32x4 x = ring[stage][T::BW * 8 + place];
+#pragma unroll
+        for (int i = 0; i < T::TW; ++i)
+            acc[i] = mfma32<STEP>(ring[stage][256 * i + place], scales[i], x, scales[T::TW], acc[i]);
+    }
+};
+
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void k_mx4_long(Mx4 x, int rows, Mx4 w, int out, int blocks,
+                                                          void* __restrict__ y, int y_bf16, int64_t y_stride) {
+    __shared__ u32x4 ring[T::kWaves][T::kStages][T::kLoads * 64];
+    static_assert(sizeof(ring) >= sizeof(float) * T::kWaves * T::TW * 16 * 64, "the sums fit");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int o0 = blockIdx.x * T::BW, mine_w = min(out - o0, T::BW);
+    const int xs = (int)x.code_stride, ws = (int)w.code_stride;
+    const int slices = (blocks + 7) / 8;
+    LongWave<T> t{ring[wave],
+                  __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(w.codes) + o0 * w.code_stride),
+                                                    (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
+                  __builtin_amdgcn_make_buffer_rsrc(uniform(x.codes), (short)0, (rows - 1) * xs + blocks * 16,
+                                                    0x00020000),
+                  {}, {}, blocks, (lane & 7) ^ (lane >> 4), lane >> 5};
+#pragma unroll
+    for (int u = 0; u < T::kLoads; ++u) {
+        const int row = u * 8 + lane / 8, in_x = row - T::BW, at = (t.lblock ^ (4 * (u & 1))) * 16;
+        t.from[u] = row < T::BW ? (row < mine_w ? (uint32_t)(row * ws + at) : kNowhere)
+                                : (in_x < rows ? (uint32_t)(in_x * xs + at) : kNowhere);
+    }
+#pragma unroll
+    for (int i = 0; i < T::TW; ++i)
+        t.scale_row[i] =
+            static_cast<const uint8_t*>(w.scales) + (o0 + min(32 * i + (lane & 31), mine_w - 1)) * w.scale_stride;
+    t.scale_row[T::TW] = static_cast<const uint8_t*>(x.scales) + min(lane & 31, rows - 1) * x.scale_stride;
+    f32x16 acc[T::TW];
+#pragma unroll
+    for (int i = 0; i < T::TW; ++i) acc[i] = f32x16{};
+    uint32_t scales[T::kStages][T::TW + 1];
+#pragma unroll
+    for (int i = 0; i < T::kStages; ++i) {
+        t.fetch(wave + i * T::kWaves, i, scales[i]);
+        asm volatile("" ::: "memory");
+    }
+    // a turn's codes and scales are asked for together, the oldest first
+    // (turns behind the last multiply zeros)
+    for (int slice = wave; slice < slices;) {
+#pragma unroll
+        for (int stage = 0; stage < T::kStages; ++stage) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((T::kStages - 1) * T::kTurnLoads) : "memory");
+            t.mend(slice, scales[stage]);
+            t.template step<0>(stage, lane, scales[stage], acc);
+            t.template step<1>(stage, lane, scales[stage], acc);
+            t.template step<2>(stage, lane, scales[stage], acc);
+            t.template step<3>(stage, lane, scales[stage], acc);
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the turn has been read
+            t.fetch(slice + T::kStages * T::kWaves, stage, scales[stage]);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            slice += T::kWaves;
+        }
+    }
+    arrive<0>();  // the loads behind the last turn write shared memory, too
+    float* sums = reinterpret_cast<float*>(&ring[0][0][0]);
+#pragma unroll
+    for (int i = 0; i < T::TW; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sums[((wave * T::TW + i) * 16 + e) * 64 + lane] = acc[i][e];
+    __syncthreads();
+    const int row = lane & 31;
+    if (row >= rows) return;
+    char* at = static_cast<char*>(y) + (row * y_stride + o0) * (y_bf16 ? 2 : 4);
+#pragma unroll
+    for (int q = 0; q < T::kQuarter; q += 4) {
+        const int first = wave * T::kQuarter + q, i = first / 16, e0 = first % 16;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < T::kWaves; ++k) v[e] += sums[((k * T::TW + i) * 16 + e0 + e) * 64 + lane];
+        }
+        const int col = 32 * i + 2 * e0 + 4 * t.half;
+        store4(at, y_bf16, col, v, out - o0 - col);
+    }
+}
+
+template <typename T>
+int launch_long(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
+                int64_t y_stride, hipStream_t s) {
+    k_mx4_long<T><<<(unsigned)((out + T::BW - 1) / T::BW), T::kThreads, 0, s>>>(x, (int)rows, w, (int)out,
+                                                                              (int)blocks, y, y_bf16, y_stride);
+    return (int)hipGetLastError();
+}
+
 template <int TX>
 int launch_rows(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
                 int64_t y_stride, hipStream_t s) {
@@ -525,30 +678,51 @@ int launch_rows(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t b
 }
 
 // 128 columns of y for 64 rows of x: three stages of 256 columns.
+// 32 columns of y for 32 rows of x: two turns of 256 columns in each of four waves,
+// two workgroups a compute unit. us, 28672 x 8192 with 20 rows: 26; three turns and
+// 64 columns of y 43 (half as many workgroups), four turns 27 and two waves 30. The
+// narrower tile's share of x costs where there are many: 20 rows, 8192 x 128256 123
+// against 118 with 128 columns of y in two waves, which takes 77 at 28672 x 8192.
+using LongRows = Long<1, 4, 2>;
 using Narrow = Tile<2, 1, 2, 2, 8, 3, 2>;
 // 128 for 128: four stages of 128 columns, two workgroups a compute unit.
 using Middle = Tile<2, 2, 2, 2, 4, 4, 2>;
 // 256 for 256: eight waves, the fewest bytes through shared memory a flop.
 using Wide = Tile<2, 4, 4, 2, 4, 4, 2>;
 
-enum Shape { kFew, kRows, kNarrow, kMiddle, kWide };
+enum Shape { kFew, kRows, kLong, kNarrow, kMiddle, kWide };
 
-// The shape for rows of x and out rows of W, by how many workgroups each gives the
-// 256 compute units. us, columns x rows of W:
-//   rows of x                   few  rows<2>  narrow  middle  wide
-//   1, 8192 x 128256            111      168     105     115   131
-//   16, 8192 x 28672             41       50      32      32    51   narrow from 200 tiles on
-//   16, 4096 x 4096             4.5      6.7      10      11    23
-//   20, 2048 x 11008            8.7      9.0     6.5     7.6    14   above 16 rows from 80 on
-//   20, 28672 x 8192             63       43      83      79   155
-//   64, 28672 x 8192            133       70      90      87   168
-//   77, 28672 x 8192            162       98      74      88   170   narrow up to 256 tiles
-//   192, 2048 x 11008            36       27      14      11    20
-//   256, 8192 x 28672           495      234      97      66    74   wide from 160 tiles on
-//   384, 8192 x 28672                            144      94    77
-//   1024, 2048 x 11008                            33      29    27
-Shape choose(int64_t rows, int64_t out) {
+// The shape for rows of x, out rows of W and blocks of either, by how many
+// workgroups each gives the 256 compute units. us, columns x rows of W:
+//   rows of x                   few  rows<2>  long  narrow  middle  wide
+//   1, 4096 x 4096              4.1           5.1                        up to 16 rows few below 256 tiles of 32
+//   16, 4096 x 4096             4.7      6.7  5.5      10      11    23
+//   16, 4096 x 6400             6.9           5.8
+//   1, 4096 x 11008             6.9           8.3                        (where the rule errs most)
+//   16, 8192 x 8192              13            10
+//   1, 28672 x 8192              26            21
+//   1, 8192 x 128256            111      168  101     105     115   131
+//   16, 8192 x 128256                         117     117
+//   1, 2048 x 151936                           37      35                narrow from 200 tiles of 128 on where
+//   16, 2048 x 151936                          44      38                rows are short
+//   16, 8192 x 28672             41       50   30      32      32    51
+//   20, 2048 x 11008            8.7      9.0  6.8     6.5     7.6    14  above 16 rows narrow from 200 on
+//   20, 28672 x 8192             63       43   26      83      79   155
+//   32, 4096 x 4096                      7.8  6.2
+//   32, 8192 x 28672                           35      32
+//   64, 28672 x 8192            133       70           90      87   168
+//   77, 28672 x 8192            162       98           74      88   170  narrow up to 256 tiles
+//   192, 2048 x 11008            36       27           14      11    20
+//   256, 8192 x 28672           495      234           97      66    74  wide from 160 tiles on
+//   384, 8192 x 28672                                 144      94    77
+//   1024, 2048 x 11008                                 33      29    27
+Shape choose(int64_t rows, int64_t out, int64_t blocks) {
     const int64_t narrow = (out + Narrow::BW - 1) / Narrow::BW;
+    if (rows <= 32 && blocks >= 8) {
+        if (rows > 16) return narrow >= 200 ? kNarrow : kLong;
+        if ((out + LongRows::BW - 1) / LongRows::BW < 256) return kFew;
+        return narrow >= 200 && blocks < 128 ? kNarrow : kLong;
+    }
     if (rows <= Narrow::BX) {
         if (narrow >= 200 || (rows > 16 && narrow >= 80)) return kNarrow;
         return rows <= 16 ? kFew : kRows;
@@ -568,8 +742,9 @@ int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_feat
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const int bf16 = y_dtype == ZS_DTYPE_BF16;
     const bool tiled = blocks > 0 && x.code_stride <= kTiledStride && w.code_stride <= kTiledStride;
-    switch (tiled ? choose(rows, out_features) : kFew) {
+    switch (tiled ? choose(rows, out_features, blocks) : kFew) {
         case kRows: return launch_rows<2>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        case kLong: return launch_long<LongRows>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kNarrow: return launch_tiled<Narrow>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kMiddle: return launch_tiled<Middle>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kWide: return launch_tiled<Wide>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
