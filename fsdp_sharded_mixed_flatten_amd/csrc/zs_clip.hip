@@ -152,17 +152,29 @@ __global__ __launch_bounds__(kNormThreads) void k_multi_norm(const MultiHeader* 
     }
 }
 
-// One workgroup: thread i adds up sums i, i + 1024, ... in order.
-constexpr int kFinalThreads = 1024;
+// One workgroup: thread i adds up sums i, i + 1024, ... in order, eight loads at a
+// time (51400 sums: 17 us one by one).
+constexpr int kFinalThreads = 1024, kFinalHeld = 8;
 __global__ __launch_bounds__(kFinalThreads) void k_multi_norm_final(const double* __restrict__ part,
                                                                     const int32_t* __restrict__ flags, int64_t n,
                                                                     double* __restrict__ sumsq_out,
                                                                     int32_t* __restrict__ nonfinite_out) {
     double s = 0.0;
     bool bad = false;
-    for (int64_t i = threadIdx.x; i < n; i += kFinalThreads) {
-        s += part[i];
-        bad |= flags[i] != 0;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kFinalThreads * kFinalHeld) {
+        double held[kFinalHeld];
+        int32_t any[kFinalHeld];
+#pragma unroll
+        for (int k = 0; k < kFinalHeld; ++k) {
+            const int64_t i = i0 + k * kFinalThreads;
+            held[k] = part[i < n ? i : i0];
+            any[k] = flags[i < n ? i : i0];
+        }
+#pragma unroll
+        for (int k = 0; k < kFinalHeld; ++k) {
+            if (i0 + k * kFinalThreads < n) s += held[k];
+            bad |= any[k] != 0;
+        }
     }
     group_sum<kFinalThreads / 64>(s, bad);
     if (threadIdx.x == 0) {
