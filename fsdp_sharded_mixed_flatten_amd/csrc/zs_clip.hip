@@ -76,7 +76,10 @@ __device__ __forceinline__ void group_sum(double& s, bool& bad) {
 
 // Workgroup g adds up chunks [g * kNormChunks, (g + 1) * kNormChunks). A square
 // of a bf16 is finite in double, and so is any sum of them: a sum that is not
-// comes from an element that is not.
+// comes from an element that is not. Bound by memory: a range inside one piece is
+// streamed (842M elements 252 us, 6.7 TB/s); ranges of several pieces look theirs
+// up first, all rows of the workgroup at once (434 pieces, 48M elements 19 us, 5.1
+// TB/s). With a lookup a chunk before its load the calls took 1233 and 78 us.
 __global__ __launch_bounds__(kNormThreads) void k_multi_norm(const MultiHeader* __restrict__ hdr, MultiOffsets moff,
                                                              int64_t unsummed, int64_t n_chunks,
                                                              double* __restrict__ part, int32_t* __restrict__ flags) {
@@ -221,7 +224,8 @@ __device__ __forceinline__ void st_lane(T* p, T x) {
 }
 
 // One chunk (four elements a lane) a workgroup of one wave, as the unclipped
-// multi-tensor step.
+// multi-tensor step. Bound by memory, 28 bytes an element: 193M elements 827 us,
+// 6.6 TB/s.
 constexpr unsigned kStepLds = 12u << 10;  // unused: fewer waves a compute unit keep fewer DRAM rows in play
 __global__ __launch_bounds__(kBlockThreads) void k_multi_clip(CoefTable ct, const MultiHeader* __restrict__ hdr,
                                                               MultiOffsets off, const float* __restrict__ scale_p,
