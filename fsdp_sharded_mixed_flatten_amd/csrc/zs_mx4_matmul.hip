@@ -236,7 +236,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_rows(Mx4 x, int rows, Mx
 // 4096 x 8192 x 28672: 541 to 565 us, 3.4 to 3.6 PFLOP/s, where the instructions
 // alone reach 6.5 on such codes and 8.7 on zeros: the card lowers its clock under
 // them, and workgroups that stay, other orders of tiles and other shapes gained
-// nothing. 20 x 8192 x 128256: 114 to 123 us, 4.8 TB/s of W read in runs of one line.
+// nothing. 20 x 8192 x 128256: 104 to 112 us, 5.2 to 5.6 TB/s; runs of two lines of
+// a row with 32 rows of x a tile take 127.
 // A lane of a 32 x 32 instruction gives one block of row l % 32. Which 64
 // columns an instruction takes is free as long as both sides agree: the lower
 // lanes take blocks 0 and 1 of a turn's four, the upper ones 2 and 3, so that a
@@ -288,11 +289,19 @@ struct Scales {
 // 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
 constexpr uint32_t kNowhere = 0x7FFFFFF0u;
 
+// Rows of W that many bytes apart, or a multiple of it, have the same columns in
+// the same part of the memory, which workgroups that all begin with a row's first
+// columns would ask at once: each begins elsewhere in its rows. us with and
+// without, 8192 columns (4096 bytes) x 128256: 1 row 89 and 99, 20 rows 112 and 124;
+// x 28672: 1 row 24 and 27. 4096 columns x 28672: 16.1 and 15.4; 12288 x 28672: 35
+// and 34; where W is read by several tiles (4096 rows of x) 583 and 563.
+constexpr int kCrowded = 4096;
+
 template <typename T>
 struct Tiled {
     Shared<T>& sh;
     __amdgpu_buffer_rsrc_t wr, xr;
-    int blocks;
+    int blocks, groups, first;  // groups of 512 columns, and the one that the tile begins with
     bool once;                  // no other tile reads this one's rows of W
     int wave, lblock;           // the block of a turn that this thread's loads take
     uint32_t from[T::kLoads];   // and where in W and x they find it in turn 0
@@ -305,9 +314,15 @@ struct Tiled {
     // the scales, whose lines are read a piece at a time (20 rows x 8192 x 128256:
     // 114 us against 125). With half lines a turn the other half would be lost.
     static constexpr int kNontemporal = 2;
+    static constexpr bool kElsewhere = T::kBlocks == 8;  // of the tiles, the narrow one may be alone over its rows of W
     static constexpr int kLoadRows = T::kThreads / T::kBlocks;
     __device__ __forceinline__ void fetch(int turn, int stage) {
-        const uint32_t add = turn * T::kBlocks + lblock < blocks ? turn * (T::kBlocks * 16u) : kNowhere;
+        int real = turn;
+        if constexpr (kElsewhere) {
+            const int turns = groups * T::kTurns, at = turn + first * T::kTurns;
+            real = turn >= turns ? turns : at - (at >= turns ? turns : 0);
+        }
+        const uint32_t add = real * T::kBlocks + lblock < blocks ? real * (T::kBlocks * 16u) : kNowhere;
 #pragma unroll
         for (int u = 0; u < T::kLoads; ++u) {
             const lds_ptr to = (lds_ptr)&sh.codes[stage][u * T::kThreads + wave * 64];
@@ -320,7 +335,9 @@ struct Tiled {
         }
     }
     // Scales of 512 columns (16 bytes a row) go through registers.
-    __device__ __forceinline__ void fetch_scales(int group) {
+    __device__ __forceinline__ void fetch_scales(int turn_group) {
+        int group = turn_group;
+        if constexpr (kElsewhere) group = group + first - (group + first >= groups ? groups : 0);
         if ((group + 1) * 16 <= blocks) {
 #pragma unroll
             for (int k = 0; k < T::kScaleLoads; ++k)
@@ -404,12 +421,13 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void k_mx4_tiled(Mx4 x, i
     const int mine_x = min(rows - r0, T::BX), mine_w = min(out - o0, T::BW);
     const int xs = (int)x.code_stride, ws = (int)w.code_stride;
     const int wave_w = wave % T::WW, wave_x = wave / T::WW;
+    const int groups = (blocks + 15) / 16;  // turns behind the last block multiply zeros
     Tiled<T> t{sh,
                __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(w.codes) + o0 * w.code_stride),
                                                  (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
                __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride),
                                                  (short)0, (mine_x - 1) * xs + blocks * 16, 0x00020000),
-               blocks, tiles_x == 1, wave, (tid & (T::kBlocks - 1)) ^ (tid >> 4 & (T::kBlocks - 1)), {},
+               blocks, groups, tiles_x == 1 && ws % kCrowded == 0 ? tile % groups : 0, tiles_x == 1, wave, (tid & (T::kBlocks - 1)) ^ (tid >> 4 & (T::kBlocks - 1)), {},
                32 * T::TW * wave_w + (lane & 31), 32 * T::TX * wave_x + (lane & 31),
                T::kBlocks == 4 ? lane >> 2 & 3 : lane >> 1 & 7,
                lane >> 5, {}, {}};
@@ -432,7 +450,6 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void k_mx4_tiled(Mx4 x, i
 #pragma unroll
         for (int j = 0; j < T::TX; ++j) acc[i][j] = f32x16{};
 
-    const int groups = (blocks + 15) / 16;  // turns behind the last block multiply zeros
     t.fetch_scales(0);
 #pragma unroll
     for (int i = 0; i < T::kStages; ++i) t.fetch(i, i);
@@ -527,8 +544,7 @@ int launch_few(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t bl
 // ------------------------------------------------------------------ few rows, many of W
 // Up to 32 rows of x, 32 TW rows of W. The workgroup's WAVES waves share a row's
 // columns, 256 each in turn, so that together they read runs of WAVES * 128 bytes
-// of a row (runs of one line take the memory longer: W laid out tile by tile would
-// stream in 96 us where the narrow tile's runs of one line take 114). A wave's
+// of a row. A wave's
 // columns are its own: codes go through its own ring of STAGES turns in shared
 // memory with waits by count and no barrier, scales through registers. At the
 // end the waves' sums are added up through shared memory.
@@ -549,19 +565,24 @@ struct LongWave {
     __amdgpu_buffer_rsrc_t wr, xr;
     const uint8_t* scale_row[T::TW + 1];
     uint32_t from[T::kLoads];
-    int blocks, lblock, half;
+    int blocks, slices, first, lblock, half;  // first: the slice of 256 columns that this workgroup begins with
 
+    // The slice of the row that the workgroup's slice number `slice` is; behind the
+    // last, what is behind the row's end.
+    __device__ __forceinline__ int place_of(int slice) const {
+        return slice >= slices ? slices : slice + first - (slice + first >= slices ? slices : 0);
+    }
     // Loads of W leave the caches to x and the scales, whose lines are read a piece
     // at a time.
     __device__ __forceinline__ void fetch(int slice, int stage, uint32_t (&scales)[T::TW + 1]) {
-        const int at_block = min(slice * 8 + 4 * half, blocks - 4);
+        const int real = place_of(slice), at_block = min(real * 8 + 4 * half, blocks - 4);
 #pragma unroll
         for (int i = 0; i <= T::TW; ++i) scales[i] = *reinterpret_cast<const u32_u1*>(scale_row[i] + at_block);
 #pragma unroll
         for (int u = 0; u < T::kLoads; ++u) {
             const lds_ptr to = (lds_ptr)&ring[stage][u * 64];
-            const int block = slice * 8 + (lblock ^ (4 * (u & 1)));
-            const uint32_t at = from[u] + (block < blocks ? slice * 128u : kNowhere);
+            const int block = real * 8 + (lblock ^ (4 * (u & 1)));
+            const uint32_t at = from[u] + (block < blocks ? real * 128u : kNowhere);
             if (u < T::kWLoads)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, (int)at, 0, 0, 2);
             else
@@ -571,7 +592,7 @@ struct LongWave {
     // Scales that reach behind the row's end were read from its last four on; what
     // lies behind is 1.
     __device__ __forceinline__ void mend(int slice, uint32_t (&scales)[T::TW + 1]) const {
-        const int over = min(max(slice * 8 + 4 * half - (blocks - 4), 0), 4);
+        const int over = min(max(place_of(slice) * 8 + 4 * half - (blocks - 4), 0), 4);
 #pragma unroll
         for (int i = 0; i <= T::TW; ++i)
             scales[i] = (uint32_t)((uint64_t(0x7F7F7F7F) << 32 | scales[i]) >> (8 * over));
@@ -602,7 +623,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx4_long(Mx4 x, int rows, Mx4 w
                                                     (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
                   __builtin_amdgcn_make_buffer_rsrc(uniform(x.codes), (short)0, (rows - 1) * xs + blocks * 16,
                                                     0x00020000),
-                  {}, {}, blocks, (lane & 7) ^ (lane >> 4), lane >> 5};
+                  {}, {}, blocks, slices, ws % kCrowded == 0 ? (int)(blockIdx.x % (unsigned)slices) : 0, (lane & 7) ^ (lane >> 4), lane >> 5};
 #pragma unroll
     for (int u = 0; u < T::kLoads; ++u) {
         const int row = u * 8 + lane / 8, in_x = row - T::BW, at = (t.lblock ^ (4 * (u & 1))) * 16;
@@ -707,11 +728,14 @@ enum Shape { kFew, kRows, kLong, kNarrow, kMiddle, kWide };
 //   1, 4096 x 11008             6.9           8.3                        (where the rule errs most)
 //   16, 8192 x 8192              13            10
 //   1, 28672 x 8192              26            21
-//   1, 8192 x 128256            111      168  101     105     115   131
-//   16, 8192 x 128256                         117     117
-//   1, 2048 x 151936                           37      35                narrow from 200 tiles of 128 on where
-//   16, 2048 x 151936                          44      38                rows are short
-//   16, 8192 x 28672             41       50   30      32      32    51
+//   1, 8192 x 128256            111      168   89     102     115   131
+//   8, 8192 x 128256                          103     106                narrow from 800 tiles of 128 on above
+//   16, 8192 x 128256                         116     111                8 rows, and where rows are short
+//   1, 4096 x 128256                           51      48
+//   16, 4096 x 128256                          63      54
+//   1, 2048 x 151936                           37      35                (of fewer than 128 blocks: from 200 on)
+//   16, 2048 x 40000                           14      13
+//   16, 8192 x 28672             41       50   28      30      32    51
 //   20, 2048 x 11008            8.7      9.0  6.8     6.5     7.6    14  above 16 rows narrow from 200 on
 //   20, 28672 x 8192             63       43   26      83      79   155
 //   32, 4096 x 4096                      7.8  6.2
@@ -727,7 +751,7 @@ Shape choose(int64_t rows, int64_t out, int64_t blocks) {
     if (rows <= 32 && blocks >= 8) {
         if (rows > 16) return narrow >= 200 ? kNarrow : kLong;
         if ((out + LongRows::BW - 1) / LongRows::BW < 256) return kFew;
-        return narrow >= 200 && blocks < 128 ? kNarrow : kLong;
+        return (narrow >= 200 && blocks < 128) || (narrow >= 800 && (blocks <= 128 || rows > 8)) ? kNarrow : kLong;
     }
     if (rows <= Narrow::BX) {
         if (narrow >= 200 || (rows > 16 && narrow >= 80)) return kNarrow;

@@ -32,6 +32,15 @@ def test_products(zs, rows, out, cols, dtype):
     _check(zs, rows, out, cols, dtype, 4, (60, 70), pad=3, shift=1, y_pad=5)
 
 
+@pytest.mark.parametrize("cols", [8192, 8161, 7700, 4096, 1000, 300])
+@pytest.mark.parametrize("rows,out", [(1, 8200), (20, 300), (9, 102500), (24, 25700), (33, 25700)])
+def test_rows_a_multiple_of_4096_bytes_apart(zs, rows, out, cols):
+    """Workgroups that begin anywhere in their rows, whole and short ones."""
+    _check(zs, rows, out, cols, "f32", cols, None, pad=256 - -(-cols // 32))
+    if out < 1000:
+        _check(zs, rows, out, cols, "f32", cols, (120, 134), pad=512 - -(-cols // 32))
+
+
 @pytest.mark.parametrize("rows,out,cols", [(20, 66, 260), (20, 66, 1100), (5, 8200, 1100), (32, 32, 2048)])
 def test_nan_blocks(zs, rows, out, cols):
     """A NaN block reaches its row or column alone, the last block of a row too; scales behind a row are not read as
