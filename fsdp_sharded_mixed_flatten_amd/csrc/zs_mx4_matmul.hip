@@ -427,7 +427,8 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void k_mx4_tiled(Mx4 x, i
                                                  (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
                __builtin_amdgcn_make_buffer_rsrc(uniform(static_cast<const char*>(x.codes) + r0 * x.code_stride),
                                                  (short)0, (mine_x - 1) * xs + blocks * 16, 0x00020000),
-               blocks, groups, tiles_x == 1 && ws % kCrowded == 0 ? tile % groups : 0, tiles_x == 1, wave, (tid & (T::kBlocks - 1)) ^ (tid >> 4 & (T::kBlocks - 1)), {},
+               blocks, groups, tiles_x == 1 && ws % kCrowded == 0 ? tile % groups : 0, tiles_x == 1, wave,
+               (tid & (T::kBlocks - 1)) ^ (tid >> 4 & (T::kBlocks - 1)), {},
                32 * T::TW * wave_w + (lane & 31), 32 * T::TX * wave_x + (lane & 31),
                T::kBlocks == 4 ? lane >> 2 & 3 : lane >> 1 & 7,
                lane >> 5, {}, {}};
@@ -623,7 +624,8 @@ __global__ __launch_bounds__(T::kThreads) void k_mx4_long(Mx4 x, int rows, Mx4 w
                                                     (short)0, (mine_w - 1) * ws + blocks * 16, 0x00020000),
                   __builtin_amdgcn_make_buffer_rsrc(uniform(x.codes), (short)0, (rows - 1) * xs + blocks * 16,
                                                     0x00020000),
-                  {}, {}, blocks, slices, ws % kCrowded == 0 ? (int)(blockIdx.x % (unsigned)slices) : 0, (lane & 7) ^ (lane >> 4), lane >> 5};
+                  {}, {}, blocks, slices, ws % kCrowded == 0 ? (int)(blockIdx.x % (unsigned)slices) : 0,
+                  (lane & 7) ^ (lane >> 4), lane >> 5};
 #pragma unroll
     for (int u = 0; u < T::kLoads; ++u) {
         const int row = u * 8 + lane / 8, in_x = row - T::BW, at = (t.lblock ^ (4 * (u & 1))) * 16;
