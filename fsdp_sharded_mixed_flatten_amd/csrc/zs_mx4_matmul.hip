@@ -20,30 +20,25 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the matrix instructions' name of the format
 
-// Round to nearest even, the only rounding of a result; NaN stays NaN.
-__device__ __forceinline__ uint16_t f32_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    return (uint16_t)(((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r);
+// Two results as bf16 in one word: the hardware's conversion, which rounds to
+// nearest even (compared with the rounding by integers over all 2^32 fp32 values:
+// no bit differs), the only rounding of a result; NaN stays NaN.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
 __device__ __forceinline__ void store_y(void* y, bool bf16, int64_t i, float v) {
     if (bf16)
-        static_cast<uint16_t*>(y)[i] = f32_bf16(v);
+        static_cast<uint16_t*>(y)[i] = (uint16_t)pack_bf16(v, v);
     else
         static_cast<float*>(y)[i] = v;
 }
 
 // Four results side by side, `left` of which there are, k elements behind `at`.
-// The hardware's conversion rounds to nearest even but for one value in 2^17 next
-// to a tie, half a step and 2^-16 of one off.
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_u2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_u4 __attribute__((ext_vector_type(4), aligned(4)));
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
 __device__ __forceinline__ void store4(char* at, bool bf16, int k, const float (&v)[4], int left) {
     if (left >= 4) {
         if (bf16)
