@@ -280,8 +280,9 @@ struct Scales {
 };
 
 // What a load leaves out (rows past the end, blocks past the last) is asked
-// for behind the buffer's end, where a load gives 0. Buffers are shorter than
-// 2^30 bytes and offsets inside them too, so that no sum passes 2^32.
+// for behind the buffer's end, where a load gives 0. Buffers are of at most 2^30
+// bytes (256 rows of 2^22), offsets inside them are smaller, and a sum of two such
+// places is below 2^32.
 constexpr uint32_t kNowhere = 0x7FFFFFF0u;
 
 // Rows of W that many bytes apart, or a multiple of it, have the same columns in
@@ -759,7 +760,7 @@ Shape choose(int64_t rows, int64_t out, int64_t blocks) {
     return ((rows + Narrow::BX - 1) / Narrow::BX) * narrow <= 256 ? kNarrow : kMiddle;
 }
 
-// Offsets in a tile stay below 2^30: 256 rows of 2^22 bytes (2^23 columns).
+// A tile spans at most 2^30 bytes: 256 rows of 2^22 (2^23 columns).
 constexpr int64_t kTiledStride = int64_t(1) << 22;
 
 }  // namespace
