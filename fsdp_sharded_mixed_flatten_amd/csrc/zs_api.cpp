@@ -1110,6 +1110,7 @@ namespace zs {
 
 zs_status bound_tables(const zs_plan* plan, const void* workspace, int32_t need, BoundTables* out) {
     if (zs_status st = check_multi_plan(plan)) return st;
+    if (plan->chunk_piece.empty()) need = 0;  // no element: its binding has no field
     Binding b;
     if (zs_status st = lookup_binding(plan, workspace, need, &b)) return st;
     out->off = multi_offsets(plan, b.n_contribs);

@@ -18,16 +18,20 @@ struct BoundTables {
 };
 
 // zs_api.cpp: the tables of the binding in a workspace, after checking that it
-// is of this plan and has the fields of `need` (MultiFlags); the coefficients of
-// each group's hyperparameters.
+// is of this plan and, unless the plan has no element, has the fields of `need`
+// (MultiFlags); the coefficients of each group's hyperparameters.
 zs_status bound_tables(const zs_plan* plan, const void* workspace, int32_t need, BoundTables* out);
 zs_status group_coefs(const zs_plan* plan, const zs_adamw_hparams* hps, int32_t n_groups, CoefTable* ct);
 
 // Chunks (kChunkElems elements each) that one workgroup of the norm adds up, and
-// the bytes of the workgroups' sums and flags.
+// the bytes of the workgroups' sums and flags (of a plan without elements: some,
+// so that a workspace has an address).
 constexpr int64_t kNormChunks = 64;
 inline int64_t norm_groups(int64_t n_chunks) { return (n_chunks + kNormChunks - 1) / kNormChunks; }
-inline int64_t norm_bytes(int64_t n_chunks) { return (norm_groups(n_chunks) * 12 + 255) / 256 * 256; }
+inline int64_t norm_bytes(int64_t n_chunks) {
+    const int64_t n = norm_groups(n_chunks);
+    return ((n > 0 ? n : 1) * 12 + 255) / 256 * 256;
+}
 
 // Launchers; they return a hipError_t value cast to int.
 int launch_multi_norm(const void* workspace, const BoundTables& t, int64_t n_chunks, double* sumsq_out,

@@ -33,7 +33,8 @@ int64_t zs_grad_stats_multi_workspace_bytes(const zs_plan* plan);
  * 0; both are always written. A replicated tensor, which every rank holds whole,
  * counts in the sum of rank 0 alone, so that the ranks' sums add up to the
  * squared norm of the whole gradient; its elements are looked at for the flag on
- * every rank. grad has to be bound. sumsq_out is 8-byte, nonfinite_out 4-byte
+ * every rank. grad has to be bound (a plan without elements gives 0 and 0).
+ * sumsq_out is 8-byte, nonfinite_out 4-byte
  * aligned; stats_workspace 16-byte, owned by the call while it is in flight, and
  * holding nothing between calls. The three overlap neither each other nor
  * `workspace`. */
@@ -43,7 +44,8 @@ zs_status zs_grad_stats_multi(const zs_plan* plan, const void* workspace, double
 /* zs_adamw_shard_step_multi_groups with element gradient f32(grad) * *scale
  * (one fp32 product; scale NULL: 1), writing param and full where they are
  * bound. If skip is non-NULL and *skip != 0 nothing is written. scale and skip
- * are device pointers. grad, master, m and v have to be bound. */
+ * are device pointers. grad, master, m and v have to be bound, unless the plan
+ * has no elements. */
 zs_status zs_adamw_shard_step_multi_clip(const zs_plan* plan, const zs_adamw_hparams* hps, int32_t n_groups,
                                          const float* scale, const int32_t* skip, const void* workspace,
                                          void* stream);
