@@ -12,7 +12,11 @@
  *   zs_adamw_shard_step_multi_clip   the step
  *
  * Conventions are those of zs.h. Factor and skip stay on the device, and every
- * call may be captured into a HIP graph.
+ * call may be captured into a HIP graph. A replay follows the gradient, the
+ * factor and the skip; the step's hyperparameters are passed by value, so that it
+ * repeats the step count and the learning rate of the call that was captured: a
+ * training loop captures the norm and the factor and makes the step's call anew
+ * (scalars in device memory are taken by the _dc calls of zs.h alone).
  */
 #ifndef ZS_CLIP_H
 #define ZS_CLIP_H

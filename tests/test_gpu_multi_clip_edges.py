@@ -1,7 +1,10 @@
-"""The clipped multi-tensor step where there is nothing to step."""
+"""The clipped multi-tensor step where there is nothing to step, and what a captured one repeats."""
+import numpy as np
 import pytest
 
-from test_gpu_multi_clip import _hp, zs  # noqa: F401  (the fixture)
+import oracle
+from gpu_util import dev16
+from test_gpu_multi_clip import Run, _hp, _sizes, zs  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +45,63 @@ def test_other_plans_still_need_their_fields(zs):
             zs.zs_adamw_shard_step_multi_clip(plan, [_hp(zs)], ws)
         assert e.value.status == zs.ZS_EINVAL
         zs.zs_multi_unbind(ws)
+
+
+def test_replays_follow_the_gradient_and_skip(zs):
+    """Every replay of a captured norm, factor and step against the eager calls: norm, flag, factor, skip and every
+    element, where a replay's gradient is finite and where it is not."""
+    import torch
+    a, b = Run(zs, _sizes(), 4, 1, 21, 300), Run(zs, _sizes(), 4, 1, 21, 300)
+    out = {r: (torch.empty(1, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")) for r in (a, b)}
+
+    def step(r):
+        r.norm()
+        zs.zs_clip_scale(r.sumsq, r.flag, 0.1, *out[r])
+        zs.zs_adamw_shard_step_multi_clip(r.plan, [_hp(zs)], r.ws, scale=out[r][0], skip=out[r][1])
+
+    for r in (a, b):
+        step(r)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(a)
+    rng = np.random.default_rng(5)
+    for k in range(5):
+        for i, o in enumerate(a.o):
+            bits = oracle.f32_to_bf16(np.float32(rng.standard_normal(o["g"].size)))
+            if k in (1, 3) and i == 0:
+                bits[7] = 0x7F80 if k == 1 else 0x7FC0
+            if bits.size:
+                for r in (a, b):
+                    r.pieces[i]["grad"].copy_(dev16(bits))
+        before = a.pieces[0]["master"].clone()
+        g.replay()
+        step(b)
+        torch.cuda.synchronize()
+        bad = k in (1, 3)
+        assert int(out[a][1]) == int(out[b][1]) == int(a.flag) == int(b.flag) == bad
+        assert torch.equal(before, a.pieces[0]["master"]) == bad
+        if not bad:
+            assert float(a.sumsq) == float(b.sumsq) and float(out[a][0]) == float(out[b][0])
+        for x, y in zip(a.pieces, b.pieces):
+            assert all(torch.equal(x[name], y[name]) for name in x)
+
+
+def test_a_captured_step_keeps_its_hyperparameters(zs):
+    """Step count and learning rate are passed by value: every replay repeats those of the capture."""
+    import torch
+    a, b = Run(zs, [5000, 300], 2, 1, 31), Run(zs, [5000, 300], 2, 1, 31)
+    g = torch.cuda.CUDAGraph()
+    hp = _hp(zs, step=3, lr=1e-3)
+    zs.zs_adamw_shard_step_multi_clip(a.plan, [hp], a.ws)
+    zs.zs_adamw_shard_step_multi_clip(b.plan, [hp], b.ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        zs.zs_adamw_shard_step_multi_clip(a.plan, [hp], a.ws)
+    hp.step, hp.lr = 100, 5e-2  # the structure was read by the call
+    for _ in range(3):
+        g.replay()
+        zs.zs_adamw_shard_step_multi_clip(b.plan, [_hp(zs, step=3, lr=1e-3)], b.ws)
+        torch.cuda.synchronize()
+        for x, y in zip(a.pieces, b.pieces):
+            assert all(torch.equal(x[name], y[name]) for name in x)
