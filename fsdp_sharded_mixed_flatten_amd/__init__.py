@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels. Functions carry the C ABI's names (``include/zs.h``, ``include/zs_clip.h``, ``include/zs_lm.h``,
-``include/zs_mx4.h``, ``include/zs_drafts.h``). Device buffers are PyTorch CUDA tensors (or raw integer device addresses); the stream is
+``include/zs_mx4.h``, ``include/zs_drafts.h``). Device buffers are PyTorch CUDA tensors (flat buffers of the step and the
+quantized gather's payload may be raw integer device addresses; workspaces, matrices and scalars are tensors, since
+their lengths and devices are looked at); the stream is
 ``torch.cuda.current_stream()`` unless one is given. Before each call the
 binding checks that every tensor is a contiguous CUDA tensor of the right
 dtype and at least as long as the kernels will touch, so a wrong shape is a
@@ -707,7 +709,7 @@ def zs_grad_stats_multi(plan, sumsq_out, nonfinite_out, workspace, stats_workspa
     _lm_call(_lib.zs_grad_stats_multi, device, stream, plan.handle, workspace.data_ptr(),
              _scalar_on(device, sumsq_out, "float64", "sumsq_out"),
              _scalar_on(device, nonfinite_out, "int32", "nonfinite_out"),
-             _lm_flat(stats_workspace, (_torch.uint8,), 0, device, "stats_workspace"), stats_workspace.numel())
+             *_lm_workspace(stats_workspace, device, "stats_workspace"))
 
 
 def zs_adamw_shard_step_multi_clip(plan, hps, workspace, scale=None, skip=None, stream=None):
@@ -835,6 +837,13 @@ def _lm_flat(t, dtypes, need, device, what):
         raise ValueError(f"{what} must hold at least {need} contiguous elements of {dtypes[0]}, got {t.numel()} of "
                          f"{t.dtype}")
     return t.data_ptr()
+
+
+def _lm_workspace(t, device, what):
+    """(address, bytes) of a workspace, whose size the library checks: an address alone does not tell it."""
+    if not isinstance(t, _torch.Tensor):
+        raise ValueError(f"{what} must be a CUDA uint8 tensor, got {type(t).__name__}")
+    return _lm_flat(t, (_torch.uint8,), 0, device, what), t.numel()
 
 
 def _lm_call(fn, device, stream, *args):
@@ -1056,7 +1065,7 @@ def zs_verify_drafts(target_logits, draft_tokens, uniforms, accepted, tokens, wo
              _lm_array(accepted, i32, requests, 0, device, "accepted"),
              _lm_array(tokens, i32, places, drafts + 1, device, "tokens"),
              _lm_array(logprobs, f32, places, drafts + 1, device, "logprobs"),
-             _lm_flat(workspace, (_torch.uint8,), 0, device, "workspace"), workspace.numel())
+             *_lm_workspace(workspace, device, "workspace"))
 
 
 def zs_last_error():
