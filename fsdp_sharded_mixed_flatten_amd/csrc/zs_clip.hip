@@ -6,29 +6,10 @@
 #include <hip/hip_runtime.h>
 
 #include "zs_clip_internal.h"
+#include "zs_device.h"
 
 namespace zs {
 namespace {
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// Pointers read from a device table are generic to the compiler, which would
-// emit flat accesses for them; every buffer here is global memory.
-template <typename T>
-using gptr = __attribute__((address_space(1))) T*;
-template <typename T>
-__device__ __forceinline__ T ld_nt(const T* p) {
-    return __builtin_nontemporal_load((gptr<const T>)p);
-}
-template <typename T>
-__device__ __forceinline__ T ld_g(const T* p) {
-    return *(gptr<const T>)p;
-}
-
-__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // ------------------------------------------------------------------ the norm
 
@@ -46,12 +27,6 @@ __device__ __forceinline__ double squares(const u32x4& v, double s) {
         s = fma(b, b, s);
     }
     return s;
-}
-
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d, 64);
-    return x;
 }
 
 // Sum and flag of a workgroup of WAVES waves, in thread 0.
@@ -188,43 +163,9 @@ __global__ __launch_bounds__(kFinalThreads) void k_multi_norm_final(const double
 
 // ------------------------------------------------------------------ the step
 
-// Round to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-    const uint32_t u = __float_as_uint(f);
-    const uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    return ((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r;
-}
-
-// The element arithmetic of zs_adamw_shard_step, operation by operation in its
-// order (fp32, one rounding each): the two steps give the same bits where the
-// factor is 1.
-__device__ __forceinline__ void adamw(const AdamCoef& c, float g, float& w, float& m, float& v) {
-    const float wd = w * c.decay;
-    m = c.b1 * m + c.omb1 * g;
-    v = c.b2 * v + c.omb2 * (g * g);
-    w = wd - c.lr * ((m / c.bc1) / (sqrtf(v / c.bc2) + c.eps));
-}
-
-// Stores of a row that the whole wave writes: a buffer resource at the row's
-// first unit, whose access carries the nontemporal policy with sc1, which a
-// global store cannot (3-4% faster than nontemporal alone in the unclipped step).
-constexpr int kBufferWord3 = 0x00020000, kStreamAux = 2 | 16;
-template <typename T>
-__device__ __forceinline__ void st_lane(T* p, T x) {
-    const uintptr_t row = reinterpret_cast<uintptr_t>(p - threadIdx.x);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)row);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(row >> 32));
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<void*>(((uintptr_t)hi << 32) | lo), (short)0, kBlockThreads * (int)sizeof(T), kBufferWord3);
-    const int off = (int)(threadIdx.x * sizeof(T));
-    if constexpr (sizeof(T) == 16)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, kStreamAux);
-    else
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, off, 0, kStreamAux);
-}
-
 // One chunk (four elements a lane) a workgroup of one wave, as the unclipped
-// multi-tensor step. Bound by memory, 28 bytes an element: 193M elements 827 us,
+// multi-tensor step, with the same element arithmetic: without a factor the bits
+// are the same. Bound by memory, 28 bytes an element: 193M elements 823 us,
 // 6.6 TB/s.
 constexpr unsigned kStepLds = 12u << 10;  // unused: fewer waves a compute unit keep fewer DRAM rows in play
 __global__ __launch_bounds__(kBlockThreads) void k_multi_clip(CoefTable ct, const MultiHeader* __restrict__ hdr,
@@ -248,7 +189,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_multi_clip(CoefTable ct, cons
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float we = w[e], me = m[e], ve = v[e];
-        adamw(c, ge[e] * scale, we, me, ve);
+        adamw_elem(c, ge[e] * scale, we, me, ve);
         w[e] = we;
         m[e] = me;
         v[e] = ve;
@@ -256,7 +197,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_multi_clip(CoefTable ct, cons
     st_lane(reinterpret_cast<f32x4*>(pc.master) + u, w);
     st_lane(reinterpret_cast<f32x4*>(pc.m) + u, m);
     st_lane(reinterpret_cast<f32x4*>(pc.v) + u, v);
-    const u32x2 p{bf16_rne(w[0]) | (bf16_rne(w[1]) << 16), bf16_rne(w[2]) | (bf16_rne(w[3]) << 16)};
+    const u32x2 p = to_bf16x4(w);
     if (hdr->flags & kHasParam) st_lane(reinterpret_cast<u32x2*>(pc.param) + u, p);
     if (hdr->flags & kHasFull) st_lane(reinterpret_cast<u32x2*>(pc.full_own) + u, p);
 }
