@@ -141,13 +141,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4 x, int64_t rows,
     }
 }
 
-// Up to 32 TX rows of x, 32 rows of W: the waves of a workgroup take turns of 512
+// Up to 64 rows of x, 32 rows of W: the waves of a workgroup take turns of 512
 // columns, whose operands they hold in registers (eight instructions of 64
 // columns, of which a lane of the upper half gives the second block), and add up
 // through shared memory.
-template <int TX>
+constexpr int kRowsX = 64;
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_rows(Mx4 x, int rows, Mx4 w, int out, int blocks,
                                                              void* __restrict__ y, int y_bf16, int64_t y_stride) {
+    constexpr int TX = kRowsX / 32;
     __shared__ float part[kFewWaves][16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
     const int r0 = blockIdx.y * 32 * TX, o0 = blockIdx.x * 32;
@@ -694,11 +695,10 @@ int launch_long(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t b
     return (int)hipGetLastError();
 }
 
-template <int TX>
 int launch_rows(const Mx4& x, int64_t rows, const Mx4& w, int64_t out, int64_t blocks, void* y, int y_bf16,
                 int64_t y_stride, hipStream_t s) {
-    k_mx4_rows<TX><<<dim3((unsigned)((out + 31) / 32), (unsigned)((rows + 32 * TX - 1) / (32 * TX))), 64 * kFewWaves, 0,
-                     s>>>(x, (int)rows, w, (int)out, (int)blocks, y, y_bf16, y_stride);
+    k_mx4_rows<<<dim3((unsigned)((out + 31) / 32), (unsigned)((rows + kRowsX - 1) / kRowsX)), 64 * kFewWaves, 0, s>>>(
+        x, (int)rows, w, (int)out, (int)blocks, y, y_bf16, y_stride);
     return (int)hipGetLastError();
 }
 
@@ -771,7 +771,7 @@ int launch_mx4_matmul(const Mx4& x, int64_t rows, const Mx4& w, int64_t out_feat
     const int bf16 = y_dtype == ZS_DTYPE_BF16;
     const bool tiled = blocks > 0 && x.code_stride <= kTiledStride && w.code_stride <= kTiledStride;
     switch (tiled ? choose(rows, out_features, blocks) : kFew) {
-        case kRows: return launch_rows<2>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
+        case kRows: return launch_rows(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kLong: return launch_long<LongRows>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kNarrow: return launch_tiled<Narrow>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
         case kMiddle: return launch_tiled<Middle>(x, rows, w, out_features, blocks, y, bf16, y_stride, s);
