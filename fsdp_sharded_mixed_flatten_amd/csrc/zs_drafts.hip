@@ -168,9 +168,10 @@ __host__ __device__ inline int64_t groups_of(int64_t pieces) { return (pieces + 
 
 // Workgroup (group, row): a wave holds its piece in registers between the
 // maximum and the sum. An element takes about 20 vector instructions, most of them
-// of 64 bits at the rate of 32-bit ones, 44 us of the 62 to 74 that 576 rows of
-// 151936 fp32 take (350 MB, 55 us at a copy's rate): memory and arithmetic are
-// both near their limit (nontemporal loads make no difference).
+// of 64 bits at the rate of 32-bit ones, whatever its type. 576 rows of 151936 fp32
+// (350 MB, 55 us at a copy's rate) take 62 to 81 us, of whose cycles the vector
+// unit is busy 67%: memory and arithmetic are both near their limit (nontemporal
+// loads make no difference). Of bf16, half the bytes, a call takes as long.
 template <typename T, int kPiece>
 __global__ __launch_bounds__(kThreads) void k_verify_rows(VerifyArgs a, Scale scale, int64_t row0,
                                                           int64_t pieces, VerifyPart* __restrict__ parts) {
@@ -261,7 +262,9 @@ struct Softmax {
 // Workgroup (group, request). Every one of a request finds out by itself how
 // many tokens stand; the first writes it down. 64 requests of 151936 fp32: 24 us,
 // of which 3 pass before the first logit is asked for (which row it is follows
-// from the sums) and 12 are two rows' bytes; one request of 32000 bf16: 7.
+// from the sums) and 12 are two rows' bytes; one request of 32000 bf16: 7. What the
+// workgroups of a request repeat grows with the square of the vocabulary: calls of
+// one request with 4 drafts take 15 us at 2^17 logits, 45 at 2^20, 450 at 2^24.
 template <typename T, int kPiece>
 __global__ __launch_bounds__(kThreads) void k_verify_rest(VerifyArgs a, Scale scale,
                                                           int64_t request0, int64_t pieces,

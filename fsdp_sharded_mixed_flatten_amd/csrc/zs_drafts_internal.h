@@ -11,11 +11,14 @@ namespace zs {
 
 // Logits of a row that one wave sums: large pieces where there are many of them,
 // small ones where waves are few and each one's time counts, and for short rows.
-// us of a call with 4 drafts in bf16, large and small pieces:
-//   1 x 32000    25  12     1 x 151936   15  17    256 x 32000    84 102
-//   8 x 32000    27  16     4 x 151936   25  21    16 x 100000    38  32
-//   64 x 32000   41  34     8 x 151936   30  30    32 x 65536     34  34
-//   128 x 32000  56  58    16 x 151936   40  44    300 x 500      30  17 (2 drafts)
+// us of a call with 4 drafts in bf16 in a graph, large and small pieces:
+//   1 x 32000    24  14     1 x 151936   23  18    256 x 32000    95 113
+//   8 x 32000    30  17     4 x 151936   28  24    16 x 100000    39  33
+//   64 x 32000   44  36     8 x 151936   32  31    32 x 65536     37  37
+//   128 x 32000  61  63     16 x 151936  43  47    64 x 151936   101 144
+// Without drafts 1 x 32000 16 and 11, 64 x 151936 23 and 37; 300 x 500 (2 drafts)
+// has a piece a row either way. The rule errs most at 64 x 32000, whose 11520 pieces
+// are large, and at 64 x 151936 without drafts, whose 4800 are not.
 constexpr int32_t kVerifyPiece = 2048, kVerifySmallPiece = 512;
 constexpr int64_t kVerifyManyPieces = 8192;
 

@@ -229,11 +229,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_rows(Mx4 x, int rows, Mx
 // bytes are four 16-byte blocks; block c of row r lies at place c ^ (r / 4 % 4),
 // so that the sixteen lanes that are served together reach all banks. (The narrow
 // tile's turn is 256 columns, eight blocks: place c ^ (r / 2 % 8).)
-// 4096 x 8192 x 28672: 541 to 565 us, 3.4 to 3.6 PFLOP/s, where the instructions
-// alone reach 6.5 on such codes and 8.7 on zeros: the card lowers its clock under
-// them, and workgroups that stay, other orders of tiles and other shapes gained
-// nothing. 20 x 8192 x 128256: 104 to 112 us, 5.2 to 5.6 TB/s; runs of two lines of
-// a row with 32 rows of x a tile take 127.
+// 4096 x 8192 x 28672: 541 to 565 us, 3.4 to 3.6 PFLOP/s, where a loop of the
+// instructions alone reaches 6.5 on such codes (8.7 on zeros). The matrix unit is
+// busy 46% of the cycles (1.64 GHz while counted; that loop 91% at 1.71 GHz), 57%
+// with no global load, and no access to shared memory conflicts: it waits for the
+// workgroup itself, one a compute unit, whose eight waves meet at a barrier every
+// 128 columns and then all read operands. 20 x 8192 x 128256: 104 to 112 us, 5.2 to
+// 5.6 TB/s; runs of two lines of a row with 32 rows of x a tile take 127.
 // A lane of a 32 x 32 instruction gives one block of row l % 32. Which 64
 // columns an instruction takes is free as long as both sides agree: the lower
 // lanes take blocks 0 and 1 of a turn's four, the upper ones 2 and 3, so that a
@@ -288,10 +290,16 @@ constexpr uint32_t kNowhere = 0x7FFFFFF0u;
 
 // Rows of W that many bytes apart, or a multiple of it, have the same columns in
 // the same part of the memory, which workgroups that all begin with a row's first
-// columns would ask at once: each begins elsewhere in its rows. us with and
-// without, 8192 columns (4096 bytes) x 128256: 1 row 89 and 99, 20 rows 112 and 124;
-// x 28672: 1 row 24 and 27. 4096 columns x 28672: 16.1 and 15.4; 12288 x 28672: 35
-// and 34; where W is read by several tiles (4096 rows of x) 583 and 563.
+// columns would ask at once: each begins elsewhere in its rows. us with and without:
+//   bytes apart         4096        8192       12288      16384      32768
+//   1 x 8192 rows    9.5  10.5   16.3 17.2   18.9 22.1   23.7 33.9   42.9 58.4
+//   20 x 8192         10  10.8   18.8 18.3   23.9 25.3   28.1 36.3   51.9 61.7
+//   1 x 28672       24.4  27.4   47.5 51.4   64.5 68.1   79.9  102    154  171
+//   20 x 28672      31.6  32.2   55.4 57.4   83.8 95.7    101  112    203  209
+//   1 x 128256        88  99.2    171  192    255  266    319  401
+//   20 x 128256      108   115    180  213    279  300    332  382
+// Where rows are 2048 or 6144 bytes apart it costs: 1 x 28672 16.1 and 15.4, 35 and
+// 34; and where W is read by several tiles (4096 rows of x) 583 and 563.
 constexpr int kCrowded = 4096;
 
 template <typename T>
@@ -712,26 +720,42 @@ using LongRows = Long<1, 4, 2>;
 using Narrow = Tile<2, 1, 2, 2, 8, 3, 2>;
 // 128 for 128: four stages of 128 columns, two workgroups a compute unit.
 using Middle = Tile<2, 2, 2, 2, 4, 4, 2>;
-// 256 for 256: eight waves, the fewest bytes through shared memory a flop.
+// 256 for 256: eight waves, each of which reads six operands for eight instructions
+// (four for four in the tile above, three for two in the narrow one).
 using Wide = Tile<2, 4, 4, 2, 4, 4, 2>;
 
 enum Shape { kFew, kRows, kLong, kNarrow, kMiddle, kWide };
 
 // The shape for rows of x, out rows of W and blocks of either, by how many
 // workgroups each gives the 256 compute units. us, columns x rows of W:
-//   rows of x                   few  rows<2>  long  narrow  middle  wide
+//   rows of x                   few  rows     long  narrow  middle  wide
 //   1, 4096 x 4096              4.1           5.1                        up to 16 rows few below 256 tiles of 32
 //   16, 4096 x 4096             4.7      6.7  5.5      10      11    23
 //   16, 4096 x 6400             6.9           5.8
-//   1, 4096 x 11008             6.9           8.3                        (where the rule errs most)
+//   1, 4096 x 11008             6.9           8.3
+//   16, 8192 x 6400              13           9.2
+//   16, 16384 x 6400             24            16                        (where the rule errs most)
 //   16, 8192 x 8192              13            10
 //   1, 28672 x 8192              26            21
 //   1, 8192 x 128256            111      168   89     102     115   131
 //   8, 8192 x 128256                          103     106                narrow from 800 tiles of 128 on above
-//   16, 8192 x 128256                         116     111                8 rows, and where rows are short
+//   16, 8192 x 128256                         117     105                8 rows, and where rows are short
+//   1, 8192 x 76800                            56      82
+//   8, 8192 x 102400                           82      95                (800 tiles)
+//   16, 8192 x 102400                          93      97
+//   16, 8192 x 51200                           49      47
+//   1, 16384 x 128256                         171     167
+//   16, 16384 x 128256                        218     178
+//   16, 16384 x 51200                          96      83
+//   1, 4096 x 76800                            33      39
+//   1, 4096 x 102400                           42      44
 //   1, 4096 x 128256                           51      48
 //   16, 4096 x 128256                          63      54
-//   1, 2048 x 151936                           37      35                (of fewer than 128 blocks: from 200 on)
+//   1, 4096 x 151936                           59      63
+//   16, 4096 x 151936                          73      70
+//   1, 2048 x 28672                            11      10                (of fewer than 128 blocks: from 200 on)
+//   1, 2048 x 76800                            22      22
+//   1, 2048 x 151936                           38      35
 //   16, 2048 x 40000                           14      13
 //   16, 8192 x 28672             41       50   28      30      32    51
 //   20, 2048 x 11008            8.7      9.0  6.8     6.5     7.6    14  above 16 rows narrow from 200 on
@@ -760,7 +784,9 @@ Shape choose(int64_t rows, int64_t out, int64_t blocks) {
     return ((rows + Narrow::BX - 1) / Narrow::BX) * narrow <= 256 ? kNarrow : kMiddle;
 }
 
-// A tile spans at most 2^30 bytes: 256 rows of 2^22 (2^23 columns).
+// A tile spans at most 2^30 bytes: 256 rows of 2^22 (2^23 columns). Rows farther
+// apart take the shape of few rows, whatever their number: 1600 x 4096 x 1600 with
+// rows 2^22 bytes apart 25 us, 16 bytes more 83 (2064 bytes: 19).
 constexpr int64_t kTiledStride = int64_t(1) << 22;
 
 }  // namespace

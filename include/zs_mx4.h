@@ -66,9 +66,11 @@ zs_status zs_mx4_dequantize(const void* codes, int64_t codes_stride, const void*
  * and W the values of two quantized matrices of in_features columns each (their
  * last blocks are multiplied whole: zs_mx4_quantize fills them with zeros).
  * Products and sums are held in fp32 and y, bf16 or fp32 (y_dtype), is rounded
- * once. A product X * W or a sum beyond fp32's range may be infinite, and what
+ * once, to the nearest, ties to even. A product X * W or a sum beyond fp32's range may be infinite, and what
  * is below fp32's normal range may be taken as 0. A NaN block gives NaN in every
- * element of y that it takes part in.
+ * element of y that it takes part in; zeros times anything else are zeros, under
+ * any scales. Many rows are multiplied fast where the rows of both matrices' codes
+ * start at most 2^22 bytes apart.
  * rows, out_features <= 2^25, in_features <= 2^29. rows == 0 or out_features
  * == 0 does nothing, in_features == 0 gives zeros. y may not overlap any
  * input; X and W may be the same matrix. */
