@@ -17,6 +17,10 @@
  * repeats the step count and the learning rate of the call that was captured: a
  * training loop captures the norm and the factor and makes the step's call anew
  * (scalars in device memory are taken by the _dc calls of zs.h alone).
+ * Replays read the table that `workspace` then holds: bound again to the same plan
+ * and number of contributions, they follow the new pieces; unbound, the sum and
+ * the flag are 0 and nothing is stepped. Bound to anything else, the graph has to
+ * be captured again.
  */
 #ifndef ZS_CLIP_H
 #define ZS_CLIP_H

@@ -105,3 +105,50 @@ def test_a_captured_step_keeps_its_hyperparameters(zs):
         torch.cuda.synchronize()
         for x, y in zip(a.pieces, b.pieces):
             assert all(torch.equal(x[name], y[name]) for name in x)
+
+
+def test_replays_follow_the_table(zs):
+    """A captured norm and step after the workspace was bound to other pieces, and after it was unbound."""
+    import torch
+    plan = zs.zs_shard_plan_ex([4096, 24], 1, 0)
+
+    def pieces(value):
+        return [dict(grad=torch.full((n,), value, dtype=torch.bfloat16, device="cuda"),
+                     master=torch.zeros(n, device="cuda"), m=torch.zeros(n, device="cuda"),
+                     v=torch.zeros(n, device="cuda")) for n in (4096, 24)]
+
+    ws = torch.zeros(zs.zs_multi_workspace_bytes(plan, 0), dtype=torch.uint8, device="cuda")
+    stats = torch.empty(zs.zs_grad_stats_multi_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+    sumsq = torch.full((1,), 7.0, dtype=torch.float64, device="cuda")
+    flag = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+
+    def calls():
+        zs.zs_grad_stats_multi(plan, sumsq, flag, ws, stats)
+        zs.zs_adamw_shard_step_multi_clip(plan, [_hp(zs)], ws)
+
+    first, second = pieces(1.0), pieces(2.0)
+    zs.zs_multi_bind(plan, first, None, ws)
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    g.replay()
+    torch.cuda.synchronize()
+    assert float(sumsq) == 4120.0 and int(flag) == 0
+    held = [d["master"].clone() for d in first]
+    zs.zs_multi_bind(plan, second, None, ws)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert float(sumsq) == 4 * 4120.0
+    assert all(torch.equal(h, d["master"]) for h, d in zip(held, first))
+    assert all(bool((d["master"] < 0).all()) for d in second)
+    held = [d["master"].clone() for d in second]
+    zs.zs_multi_unbind(ws)
+    for _ in range(2):
+        flag.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert float(sumsq) == 0.0 and int(flag) == 0
+    assert all(torch.equal(h, d["master"]) for h, d in zip(held, second))
