@@ -231,9 +231,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_rows(Mx4 x, int rows, Mx
 // tile's turn is 256 columns, eight blocks: place c ^ (r / 2 % 8).)
 // 4096 x 8192 x 28672: 541 to 565 us, 3.4 to 3.6 PFLOP/s, where a loop of the
 // instructions alone reaches 6.5 on such codes (8.7 on zeros). The matrix unit is
-// busy 46% of the cycles (1.64 GHz while counted; that loop 91% at 1.71 GHz), 57%
-// with no global load, and no access to shared memory conflicts: it waits for the
-// workgroup itself, one a compute unit, whose eight waves meet at a barrier every
+// busy 46% of the cycles (1.64 GHz while counted; that loop 91% at 1.71 GHz), 54%
+// with twice the columns, and no access to shared memory conflicts. A form with four
+// waves came from 49 to 57% with its global loads left out: most of the waiting is
+// for the workgroup itself, one a compute unit, whose waves meet at a barrier every
 // 128 columns and then all read operands. 20 x 8192 x 128256: 104 to 112 us, 5.2 to
 // 5.6 TB/s; runs of two lines of a row with 32 rows of x a tile take 127.
 // A lane of a 32 x 32 instruction gives one block of row l % 32. Which 64
